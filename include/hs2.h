@@ -385,6 +385,122 @@ HS2_API hs2_status hs2_set_fault_injection(unsigned extra_arrivals, unsigned lon
 #define HS2_PHASES 8
 HS2_API hs2_status hs2_set_phase_stamps(unsigned long long* stamps, int max_ctas);
 
+/*
+ * ------------------------------------------------------- paged decode path --
+ * One decode step of a layer whose K/V cache is paged: the norm and the E4M3
+ * projection that make the new tokens' rows (hs2_add_rmsnorm, hs2_fp8_gemm),
+ * their append (hs2_paged_append), the attention over the pages
+ * (hs2_paged_attn) and the eviction of what gathered little attention
+ * (hs2_paged_evict).  The HySparse2 pages describe none of these: they are what
+ * serving the layer needs around the calls above.
+ *
+ * A paged cache: a pool of n_pages pages of page_size positions (a power of
+ * two).  Position j of sequence b is place j % page_size of page
+ * page_table[b][j / page_size]; its slot is page * page_size + place.
+ *   kv.k, kv.v        : [n_pages][page_size][kv_heads][D], bf16 or E4M3
+ *   kv.k_scale, v_..  : fp32 [n_pages][page_size][kv_heads] for E4M3, else NULL
+ *   weight            : fp32 [n_pages][page_size], each position's accumulated
+ *                       attention weight (>= 0), or NULL where none is kept
+ *   page_table        : int32 [B][max_pages] (device); entries past a
+ *                       sequence's last page are not read
+ *   seq_len           : int32 [B] (device), 0 <= seq_len[b] <= max_pages * page_size
+ * Query heads h * G .. h * G + G - 1 read K/V head h, G = H / kv_heads.
+ * The host does not see lengths or pages: a length the table cannot hold (it is
+ * cut to the table's reach) and a page outside the pool (its positions are left
+ * out) raise HS2_ERR_DEVICE through hs2_last_device_status.  What rows behind a
+ * sequence's end hold (infinities, NaN) reaches no result.  Supported by the
+ * calls that take one: D in {64, 128}, page_size a power of two, B <= 65535,
+ * kv_heads <= 1024, n_pages * page_size < 2^31, max_pages * page_size <= 2^30;
+ * anything else is HS2_ERR_UNSUPPORTED.
+ */
+typedef struct {
+  hs2_kv_cache kv;
+  float* weight;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t max_pages;
+} hs2_paged_cache;
+
+/*
+ * hs2_add_rmsnorm -- RMS norm with the residual's addition, and an output in
+ * bf16 or in E4M3 with one scale per 128 columns (the operand layout of
+ * hs2_fp8_gemm).  For every row of T rows:
+ *   h = X + R (R NULL: h = X), in fp32
+ *   y = h * gamma / sqrt(mean(h^2) + eps)
+ *   sum = bf16(h);  Y = bf16(y)
+ *   per 128 columns: s = max|y| / 448 (1 where that is 0), Yq = E4M3(y / s)
+ * X, R, gamma, sum, Y: bf16, [T][hidden] ([hidden] for gamma); Yq: E4M3
+ * [T][hidden]; Yq_scale: fp32 [T][ceil(hidden / 128)].  sum, Y and the pair
+ * Yq, Yq_scale may be NULL, not all three; sum may be R's or X's own buffer,
+ * and Y may be X's.  hidden % 16 == 0, hidden <= 32768.
+ */
+HS2_API hs2_status hs2_add_rmsnorm(const void* X, const void* R, const void* gamma, int64_t T,
+                                   int hidden, float eps, void* sum, void* Y, void* Yq,
+                                   float* Yq_scale, hs2_stream_t stream);
+
+/*
+ * hs2_paged_append -- the new tokens' K and V rows to their pages.
+ * Sequence b's new tokens are rows row_start[b] .. row_start[b+1]-1 (int32
+ * [B + 1], device, ascending; rows outside row_start[0] .. row_start[B]-1 are
+ * not read), and they are its last positions: seq_len already counts them.
+ * row_start NULL: one new token per sequence, row b, n_rows == B.
+ *   K, V: bf16, row r's [kv_heads][D] at r * ld elements (ld >= kv_heads * D,
+ *         ld % 8 == 0: K and V may lie side by side in a projection's output).
+ *   E4M3 caches: per row and head, scale s = max|x| / 448 (1 where that is 0),
+ *         codes E4M3(x / s), round to nearest even, saturating.
+ *   weight, where kept: 0 for the new positions.
+ * A sequence with more new tokens than seq_len raises HS2_ERR_DEVICE; the
+ * surplus rows are skipped.
+ */
+HS2_API hs2_status hs2_paged_append(const void* K, const void* V, int64_t ld, int64_t n_rows,
+                                    const int32_t* row_start, const hs2_paged_cache* cache, int B,
+                                    int kv_heads, int D, hs2_kv_dtype dt, hs2_stream_t stream);
+
+/* Workspace bytes of hs2_paged_attn; 0 for sizes it would reject. */
+HS2_API size_t hs2_paged_attn_workspace(int B, int H, int kv_heads, int D);
+
+/*
+ * hs2_paged_attn -- attention of one new token per sequence over its cached
+ * positions (the new token's own row among them), split over the length and
+ * joined.  For head h of sequence b, over j < seq_len[b]:
+ *   s_hj = scale * <Q[b][h], K[j]>,  lse_h = log sum_j exp(s_hj)
+ *   O[b][h] = sum_j exp(s_hj - lse_h) V[j]
+ *   accumulate: weight_j += sum_h exp(s_hj - lse_h)  (all H heads)
+ * Q, O: bf16 [B][H][D]; lse: fp32 [B][H] or NULL.  seq_len[b] == 0: O = 0, lse =
+ * -inf.  accumulate needs cache->weight, and pages that no two sequences share
+ * (shared pages are fine without it).  H % kv_heads == 0, H / kv_heads <= 32.
+ * The workspace needs no initial value and is free again when the call's work
+ * is done.
+ */
+HS2_API hs2_status hs2_paged_attn(const void* Q, const hs2_paged_cache* cache, int B, int H,
+                                  int kv_heads, int D, float scale, hs2_kv_dtype dt, void* O,
+                                  float* lse, int accumulate, void* workspace,
+                                  size_t workspace_bytes, hs2_stream_t stream);
+
+/*
+ * hs2_paged_evict -- eviction by accumulated weight.  Sequence b of length n
+ * keeps its min(window, n) most recent positions and, of the positions before
+ * them, the min(topk, .) of largest weight (ties to the lower position, NaN
+ * below every number).  kept[b][0 .. m) lists them in ascending order, then -1
+ * (int32 [B][topk + window]); new_len[b] = m (int32 [B]; may be the cache's
+ * seq_len itself).  Position r of the sequence becomes the old position
+ * kept[b][r]: K, V, scales and weight move together.
+ *   dst_table NULL (or the cache's page_table): in place, to the sequence's
+ *     first pages; rows from m on keep what they hold.  A page whose positions
+ *     move must belong to one sequence only.
+ *   dst_table int32 [B][dst_max_pages]: into those pages of the same pool, which
+ *     must be no sequence's own; the old pages stay as they were (so they may
+ *     be shared).  dst_max_pages * page_size >= min(topk + window,
+ *     max_pages * page_size).
+ * topk >= 0, window >= 1, topk + window <= 2^24; cache->weight is needed.
+ */
+HS2_API hs2_status hs2_paged_evict(const hs2_paged_cache* cache, int B, int kv_heads, int D,
+                                   hs2_kv_dtype dt, int topk, int window,
+                                   const int32_t* dst_table, int dst_max_pages, int32_t* kept,
+                                   int32_t* new_len, hs2_stream_t stream);
+
 /* Library ABI version: 100 * major + minor. */
 HS2_API int hs2_version(void);
 

@@ -28,7 +28,8 @@ EXPORTED = ("hs2_bridge_kv", "hs2_full_attn_select_workspace", "hs2_full_attn_se
             "hs2_status_string", "hs2_version", "hs2_set_stage_events",
             "hs2_set_fault_injection", "hs2_full_attn_select_blocks", "hs2_cp_workspace",
             "hs2_cp_attn_partial", "hs2_cp_lse_combine", "hs2_cp_rescale", "hs2_cp_select_local",
-            "hs2_cp_merge_select", "hs2_set_phase_stamps")
+            "hs2_cp_merge_select", "hs2_set_phase_stamps", "hs2_add_rmsnorm",
+            "hs2_paged_append", "hs2_paged_attn", "hs2_paged_attn_workspace", "hs2_paged_evict")
 
 # Global-timer stamps per CTA written by the fused full-attention kernel when enabled.
 HS2_PHASES = 8
@@ -46,6 +47,13 @@ class Hs2Error(RuntimeError):
 class hs2_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class hs2_paged_cache(ctypes.Structure):
+    _fields_ = [("kv", hs2_kv_cache), ("weight", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
 
 
 _lib = None
@@ -103,6 +111,18 @@ def load_library(path: str = LIB_PATH):
     lib.hs2_sparse_attn.restype = i32
     lib.hs2_sparse_attn.argtypes = [P, KV, i32, i32, i64, i32, i32, ctypes.c_float, P, P, i32, i32,
                                     P, P]
+    PC = ctypes.POINTER(hs2_paged_cache)
+    lib.hs2_add_rmsnorm.restype = i32
+    lib.hs2_add_rmsnorm.argtypes = [P, P, P, i64, i32, ctypes.c_float, P, P, P, P, P]
+    lib.hs2_paged_append.restype = i32
+    lib.hs2_paged_append.argtypes = [P, P, i64, i64, P, PC, i32, i32, i32, i32, P]
+    lib.hs2_paged_attn_workspace.restype = sz
+    lib.hs2_paged_attn_workspace.argtypes = [i32, i32, i32, i32]
+    lib.hs2_paged_attn.restype = i32
+    lib.hs2_paged_attn.argtypes = [P, PC, i32, i32, i32, i32, ctypes.c_float, i32, P, P, i32, P,
+                                   sz, P]
+    lib.hs2_paged_evict.restype = i32
+    lib.hs2_paged_evict.argtypes = [PC, i32, i32, i32, i32, i32, i32, P, i32, P, P, P]
     _lib = lib
     return lib
 
@@ -267,3 +287,104 @@ def hs2_cp_merge_select(cand_score, cand_idx, G, B, T, q_pos0, topk, window, idx
     _check("hs2_cp_merge_select", load_library().hs2_cp_merge_select(
         _ptr(cand_score), _ptr(cand_idx), int(G), int(B), int(T), int(q_pos0), int(topk),
         int(window), _ptr(idx), _ptr(n_sel), _stream(stream)))
+
+
+# --------------------------------------------------- paged decode path --
+# Tensors given to these calls must be contiguous (K and V of the append excepted),
+# of the type the C ABI names, and on the current device, whose current stream the
+# work is enqueued on; anything else raises Hs2Error (invalid argument).  E4M3
+# codes are uint8 or float8_e4m3fn tensors.  Raw pointers are taken as they are.
+def _tensors(fn: str, specs):
+    """Device pointers of (tensor, element size, least elements, contiguous) entries."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    out = []
+    for t, size, least, contiguous in specs:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        if (t.get_device() != dev or t.element_size() != size or t.numel() < least
+                or (contiguous and not t.is_contiguous())):
+            raise Hs2Error(fn, 1)
+        out.append(t.data_ptr())
+    return out
+
+
+def paged_cache(k, v, page_table, seq_len, k_scale=None, v_scale=None,
+                weight=None) -> hs2_paged_cache:
+    """The C struct of a paged cache: k, v [n_pages, page_size, kv_heads, D] (bf16, or E4M3
+    with scales [n_pages, page_size, kv_heads]), page_table int32 [B, max_pages], seq_len
+    int32 [B], weight fp32 [n_pages, page_size].  Like kv_cache, it keeps its tensors."""
+    n_pages, page_size, heads, _ = k.shape
+    if (v.shape != k.shape or v.dtype != k.dtype or page_table.dim() != 2
+            or seq_len.numel() != page_table.shape[0]
+            or (k_scale is None) != (v_scale is None) or (k_scale is None) != (k.element_size() == 2)):
+        raise Hs2Error("paged_cache", 1)
+    rows = n_pages * page_size
+    p = _tensors("paged_cache", ((k, 2 if k_scale is None else 1, 1, True),
+                                 (v, 2 if k_scale is None else 1, 1, True),
+                                 (k_scale, 4, rows * heads, True), (v_scale, 4, rows * heads, True),
+                                 (weight, 4, rows, True), (page_table, 4, 1, True),
+                                 (seq_len, 4, 1, True)))
+    c = hs2_paged_cache(hs2_kv_cache(p[0], p[1], p[2], p[3]), p[4], p[5], p[6], n_pages, page_size,
+                        page_table.shape[1])
+    c._tensors = (k, v, page_table, seq_len, k_scale, v_scale, weight)
+    c._shape = (page_table.shape[0], heads, k.shape[3], 0 if k_scale is None else 1)
+    return c
+
+
+def _check_cache(fn: str, cache, B, kv_heads, D, dt):
+    # a struct made by paged_cache knows what its tensors hold
+    shape = getattr(cache, "_shape", None)
+    if shape is not None and (B > shape[0] or (kv_heads, D, dt) != shape[1:]):
+        raise Hs2Error(fn, 1)
+
+
+def hs2_add_rmsnorm(X, R, gamma, T, hidden, eps, sum=None, Y=None, Yq=None, Yq_scale=None,
+                    stream=None):
+    n = T * hidden
+    p = _tensors("hs2_add_rmsnorm", ((X, 2, n, True), (R, 2, n, True), (gamma, 2, hidden, True),
+                                     (sum, 2, n, True), (Y, 2, n, True), (Yq, 1, n, True),
+                                     (Yq_scale, 4, T * ((hidden + 127) // 128), True)))
+    _check("hs2_add_rmsnorm", load_library().hs2_add_rmsnorm(
+        p[0], p[1], p[2], T, hidden, eps, p[3], p[4], p[5], p[6], _stream(stream)))
+
+
+def hs2_paged_append(K, V, ld, n_rows, row_start, cache: hs2_paged_cache, B, kv_heads, D, dt,
+                     stream=None):
+    """K, V: the new rows, `ld` elements apart (views into a projection's output, for example)."""
+    _check_cache("hs2_paged_append", cache, B, kv_heads, D, dt)
+    n = n_rows * kv_heads * D
+    p = _tensors("hs2_paged_append", ((K, 2, n, False), (V, 2, n, False),
+                                      (row_start, 4, B + 1, True)))
+    _check("hs2_paged_append", load_library().hs2_paged_append(
+        p[0], p[1], ld, n_rows, p[2], ctypes.byref(cache), B, kv_heads, D, dt, _stream(stream)))
+
+
+def hs2_paged_attn_workspace(B, H, kv_heads, D) -> int:
+    return int(load_library().hs2_paged_attn_workspace(B, H, kv_heads, D))
+
+
+def hs2_paged_attn(Q, cache: hs2_paged_cache, B, H, kv_heads, D, scale, dt, O, lse, accumulate,
+                   workspace, workspace_bytes: int, stream=None):
+    """One new token per sequence over its pages; `accumulate` adds each position's
+    head-summed probability to the cache's weight."""
+    _check_cache("hs2_paged_attn", cache, B, kv_heads, D, dt)
+    n = B * H * D
+    p = _tensors("hs2_paged_attn", ((Q, 2, n, True), (O, 2, n, True), (lse, 4, B * H, True),
+                                    (workspace, 1, workspace_bytes, True)))
+    _check("hs2_paged_attn", load_library().hs2_paged_attn(
+        p[0], ctypes.byref(cache), B, H, kv_heads, D, scale, dt, p[1], p[2],
+        1 if accumulate else 0, p[3], workspace_bytes, _stream(stream)))
+
+
+def hs2_paged_evict(cache: hs2_paged_cache, B, kv_heads, D, dt, topk, window, dst_table, kept,
+                    new_len, stream=None):
+    """Keeps the `topk` heaviest positions and the `window` most recent ones of every sequence,
+    moved to the pages of dst_table int32 [B, n] (None: in place)."""
+    _check_cache("hs2_paged_evict", cache, B, kv_heads, D, dt)
+    p = _tensors("hs2_paged_evict", ((dst_table, 4, B, True), (kept, 4, B * (topk + window), True),
+                                     (new_len, 4, B, True)))
+    _check("hs2_paged_evict", load_library().hs2_paged_evict(
+        ctypes.byref(cache), B, kv_heads, D, dt, topk, window, p[0],
+        0 if dst_table is None else dst_table.shape[1], p[1], p[2], _stream(stream)))

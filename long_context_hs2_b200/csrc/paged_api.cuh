@@ -1,0 +1,269 @@
+// Host side of the paged decode path's entry points (see include/hs2.h):
+// argument checks, launch plans, launches.  Included by hs2_api.cu after its
+// helpers.
+#pragma once
+
+#include "add_rmsnorm.cuh"
+#include "paged_attn.cuh"
+#include "paged_cache.cuh"
+#include "paged_evict.cuh"
+
+namespace {
+
+// --------------------------------------------------------- argument checks --
+// The pool and its table: pointers, alignment, the page size, and that every
+// position and slot is a 31-bit number.
+hs2_status check_paged(const hs2_paged_cache* c, int B, int heads, int D, hs2_kv_dtype dt) {
+  if (!c || !c->kv.k || !c->kv.v || !c->page_table || !c->seq_len) return HS2_ERR_INVALID_ARG;
+  if (!aligned16(c->kv.k) || !aligned16(c->kv.v) || !aligned4(c->page_table) ||
+      !aligned4(c->seq_len) || (c->weight && !aligned4(c->weight)))
+    return HS2_ERR_INVALID_ARG;
+  if (B < 1 || heads < 1 || D < 1 || c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1)
+    return HS2_ERR_INVALID_ARG;
+  if (dt != HS2_KV_BF16 && dt != HS2_KV_FP8_E4M3) return HS2_ERR_INVALID_ARG;
+  if (dt == HS2_KV_FP8_E4M3 && (!c->kv.k_scale || !c->kv.v_scale || !aligned4(c->kv.k_scale) ||
+                                !aligned4(c->kv.v_scale)))
+    return HS2_ERR_INVALID_ARG;
+  if (!(D == 64 || D == 128) || heads > 1024 || B > 65535 ||
+      (c->page_size & (c->page_size - 1)) != 0)
+    return HS2_ERR_UNSUPPORTED;
+  if ((int64_t)c->n_pages * c->page_size > INT32_MAX ||
+      (int64_t)c->max_pages * c->page_size > (1 << 30))
+    return HS2_ERR_UNSUPPORTED;
+  return HS2_OK;
+}
+
+PagedCache paged_params(const hs2_paged_cache* c, int B, int heads, hs2_kv_dtype dt) {
+  PagedCache p;
+  p.k = static_cast<uint8_t*>(c->kv.k);
+  p.v = static_cast<uint8_t*>(c->kv.v);
+  p.k_scale = dt == HS2_KV_FP8_E4M3 ? c->kv.k_scale : nullptr;
+  p.v_scale = dt == HS2_KV_FP8_E4M3 ? c->kv.v_scale : nullptr;
+  p.weight = c->weight;
+  p.page_table = c->page_table;
+  p.seq_len = c->seq_len;
+  p.n_pages = c->n_pages;
+  p.max_pages = c->max_pages;
+  p.page_shift = __builtin_ctz((unsigned)c->page_size);
+  p.B = B;
+  p.heads = heads;
+  return p;
+}
+
+// A K or V pool as [slots][heads][D], boxes of `rows` slots of one head.
+bool make_map_pool(CUtensorMap* map, const void* base, uint64_t slots, int heads, int D, int elem,
+                   uint32_t rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t row = (cuuint64_t)D * elem;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, slots};
+  cuuint64_t strides[2] = {row, row * heads};
+  const uint32_t cols = (uint32_t)std::min(D, 128 / elem);
+  cuuint32_t box[3] = {cols, 1, rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             cols * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ----------------------------------------------------------- attention plan --
+struct PagedPlan {
+  int grid;
+  size_t off_lse, off_ml, off_o, total;
+};
+
+bool check_heads(int H, int heads) { return heads >= 1 && H >= 1 && H % heads == 0; }
+
+PagedPlan paged_plan(int B, int H, int heads, int D) {
+  PagedPlan pl;
+  pl.grid = std::min(sm_count(), kPaMaxParts);
+  const size_t G = (size_t)(H / heads);
+  pl.off_lse = 0;
+  pl.off_ml = align_up((size_t)B * H * 4, 256);
+  pl.off_o = align_up(pl.off_ml + (size_t)pl.grid * 2 * G * 8, 256);
+  pl.total = align_up(pl.off_o + (size_t)pl.grid * 2 * G * D * 4, 256);
+  return pl;
+}
+
+template <int MT, int D, bool FP8>
+hs2_status run_paged_attn(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnParams& p,
+                          bool weight, cudaStream_t s) {
+  using SM = PaSmem<MT, D, FP8, false>;
+  using SW = PaSmem<MT, D, FP8, true>;
+  auto k = paged_attn_kernel<MT, D, FP8>;
+  auto kw = paged_weight_kernel<MT, D, FP8>;
+  if (!set_smem(k, SM::kBytes)) return HS2_ERR_CUDA;
+  hs2_status st = launch(k, dim3(p.grid), dim3(kPaThreads), SM::kBytes, s, 1, km, vm, p);
+  if (st != HS2_OK) return st;
+  st = launch_ex(paged_attn_combine_kernel<D>, dim3((unsigned)(p.c.B * p.H)), dim3(D), 0, s, 1,
+                 false, true, p);
+  if (st != HS2_OK || !weight) return st;
+  if (!set_smem(kw, SW::kBytes)) return HS2_ERR_CUDA;
+  return launch_ex(kw, dim3(p.grid), dim3(kPaThreads), SW::kBytes, s, 1, false, true, km, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+hs2_status hs2_add_rmsnorm(const void* X, const void* R, const void* gamma, int64_t T, int hidden,
+                           float eps, void* sum, void* Y, void* Yq, float* Yq_scale,
+                           hs2_stream_t stream) {
+  if (!X || !gamma || (!sum && !Y && !Yq) || T < 1 || hidden < 1 || !(eps >= 0.f) ||
+      !std::isfinite(eps))
+    return HS2_ERR_INVALID_ARG;
+  if (!aligned16(X) || (R && !aligned16(R)) || !aligned16(gamma) || (sum && !aligned16(sum)) ||
+      (Y && !aligned16(Y)) || (Yq && !aligned16(Yq)))
+    return HS2_ERR_INVALID_ARG;
+  if ((Yq == nullptr) != (Yq_scale == nullptr) || (Yq_scale && !aligned4(Yq_scale)))
+    return HS2_ERR_INVALID_ARG;
+  if (hidden % kNormChunk != 0 || hidden > kNormMaxHidden || T > INT32_MAX)
+    return HS2_ERR_UNSUPPORTED;
+  NormParams p;
+  p.x = static_cast<const __nv_bfloat16*>(X);
+  p.r = static_cast<const __nv_bfloat16*>(R);
+  p.gamma = static_cast<const __nv_bfloat16*>(gamma);
+  p.sum = static_cast<__nv_bfloat16*>(sum);
+  p.y = static_cast<__nv_bfloat16*>(Y);
+  p.codes = static_cast<uint8_t*>(Yq);
+  p.scale = Yq_scale;
+  p.T = T;
+  p.hidden = hidden;
+  p.n_chunks = hidden / kNormChunk;
+  p.n_blocks = (hidden + kNormBlock - 1) / kNormBlock;
+  p.eps = eps;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (p.n_chunks <= 32)   // a warp per row, four rows per CTA
+    return launch(add_rmsnorm_kernel<1, true>, dim3((unsigned)((T + 3) / 4)), dim3(128), 0, s, 1,
+                  p);
+  const int nc = (p.n_chunks + kNormMaxThreads - 1) / kNormMaxThreads;
+  const int threads = ((p.n_chunks + nc - 1) / nc + 31) / 32 * 32;
+  auto k = nc == 1 ? add_rmsnorm_kernel<1, false>
+                   : nc == 2 ? add_rmsnorm_kernel<2, false> : add_rmsnorm_kernel<4, false>;
+  return launch(k, dim3((unsigned)T), dim3(threads), 0, s, 1, p);
+}
+
+hs2_status hs2_paged_append(const void* K, const void* V, int64_t ld, int64_t n_rows,
+                            const int32_t* row_start, const hs2_paged_cache* cache, int B,
+                            int kv_heads, int D, hs2_kv_dtype dt, hs2_stream_t stream) {
+  if (!K || !V || !aligned16(K) || !aligned16(V) || n_rows < 1 ||
+      (row_start && !aligned4(row_start)))
+    return HS2_ERR_INVALID_ARG;
+  const hs2_status st = check_paged(cache, B, kv_heads, D, dt);
+  if (st != HS2_OK) return st;
+  if (ld < (int64_t)kv_heads * D || ld % 8 != 0 || (!row_start && n_rows != B))
+    return HS2_ERR_INVALID_ARG;
+  const int64_t units = n_rows * 2 * kv_heads;
+  if (n_rows > INT32_MAX || units * (D / 8) / kAppendThreads >= INT32_MAX)
+    return HS2_ERR_UNSUPPORTED;
+  AppendParams p;
+  p.c = paged_params(cache, B, kv_heads, dt);
+  p.k = static_cast<const __nv_bfloat16*>(K);
+  p.v = static_cast<const __nv_bfloat16*>(V);
+  p.ld = ld;
+  p.row_start = row_start;
+  p.n_units = units;
+  const bool fp8 = dt == HS2_KV_FP8_E4M3;
+  auto k = D == 128 ? (fp8 ? paged_append_kernel<128, true> : paged_append_kernel<128, false>)
+                    : (fp8 ? paged_append_kernel<64, true> : paged_append_kernel<64, false>);
+  const int64_t per = kAppendThreads / (D / 8);
+  return launch(k, dim3((unsigned)((units + per - 1) / per)), dim3(kAppendThreads), 0,
+                (cudaStream_t)stream, 1, p);
+}
+
+size_t hs2_paged_attn_workspace(int B, int H, int kv_heads, int D) {
+  if (B < 1 || B > 65535 || !check_heads(H, kv_heads) || H / kv_heads > 32 || kv_heads > 1024 ||
+      !(D == 64 || D == 128) || (int64_t)B * H > INT32_MAX)
+    return 0;
+  return paged_plan(B, H, kv_heads, D).total;
+}
+
+hs2_status hs2_paged_attn(const void* Q, const hs2_paged_cache* cache, int B, int H, int kv_heads,
+                          int D, float scale, hs2_kv_dtype dt, void* O, float* lse,
+                          int accumulate, void* workspace, size_t workspace_bytes,
+                          hs2_stream_t stream) {
+  if (!Q || !O || !aligned16(Q) || !aligned16(O) || (lse && !aligned4(lse)) ||
+      !std::isfinite(scale))
+    return HS2_ERR_INVALID_ARG;
+  hs2_status st = check_paged(cache, B, kv_heads, D, dt);
+  if (st != HS2_OK) return st;
+  if (!check_heads(H, kv_heads) || (accumulate && !cache->weight)) return HS2_ERR_INVALID_ARG;
+  if (H / kv_heads > 32 || (int64_t)B * H > INT32_MAX) return HS2_ERR_UNSUPPORTED;
+  const PagedPlan pl = paged_plan(B, H, kv_heads, D);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < pl.total)
+    return HS2_ERR_WORKSPACE;
+  const bool fp8 = dt == HS2_KV_FP8_E4M3;
+  // a page's rows in a tile are one box; pages under 8 rows are not copied by
+  // TMA, and the maps then only have to be valid
+  const uint32_t rows = (uint32_t)std::min(128, std::max(8, cache->page_size));
+  const uint64_t slots = (uint64_t)cache->n_pages * cache->page_size;
+  CUtensorMap km, vm;
+  if (!make_map_pool(&km, cache->kv.k, slots, kv_heads, D, fp8 ? 1 : 2, rows) ||
+      !make_map_pool(&vm, cache->kv.v, slots, kv_heads, D, fp8 ? 1 : 2, rows))
+    return HS2_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PagedAttnParams p;
+  p.c = paged_params(cache, B, kv_heads, dt);
+  p.q = static_cast<const __nv_bfloat16*>(Q);
+  p.o = static_cast<__nv_bfloat16*>(O);
+  p.lse_out = lse;
+  p.lse = reinterpret_cast<float*>(ws + pl.off_lse);
+  p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
+  p.part_o = reinterpret_cast<float*>(ws + pl.off_o);
+  p.H = H;
+  p.G = H / kv_heads;
+  p.grid = pl.grid;
+  p.scale_log2 = scale * kPaLog2e;
+  cudaStream_t s = (cudaStream_t)stream;
+  const bool w = accumulate != 0;
+  if (p.G > 16) {
+    if (D == 128) return fp8 ? run_paged_attn<2, 128, true>(km, vm, p, w, s)
+                             : run_paged_attn<2, 128, false>(km, vm, p, w, s);
+    return fp8 ? run_paged_attn<2, 64, true>(km, vm, p, w, s)
+               : run_paged_attn<2, 64, false>(km, vm, p, w, s);
+  }
+  if (D == 128) return fp8 ? run_paged_attn<1, 128, true>(km, vm, p, w, s)
+                           : run_paged_attn<1, 128, false>(km, vm, p, w, s);
+  return fp8 ? run_paged_attn<1, 64, true>(km, vm, p, w, s)
+             : run_paged_attn<1, 64, false>(km, vm, p, w, s);
+}
+
+hs2_status hs2_paged_evict(const hs2_paged_cache* cache, int B, int kv_heads, int D,
+                           hs2_kv_dtype dt, int topk, int window, const int32_t* dst_table,
+                           int dst_max_pages, int32_t* kept, int32_t* new_len,
+                           hs2_stream_t stream) {
+  if (!kept || !new_len || !aligned4(kept) || !aligned4(new_len) ||
+      (dst_table && !aligned4(dst_table)) || topk < 0 || window < 1)
+    return HS2_ERR_INVALID_ARG;
+  const hs2_status st = check_paged(cache, B, kv_heads, D, dt);
+  if (st != HS2_OK) return st;
+  if (!cache->weight) return HS2_ERR_INVALID_ARG;
+  const int64_t reach = (int64_t)cache->max_pages * cache->page_size;
+  const int64_t most = std::min<int64_t>((int64_t)topk + window, reach);
+  if (dst_table && (dst_max_pages < 1 || (int64_t)dst_max_pages * cache->page_size < most))
+    return HS2_ERR_INVALID_ARG;
+  if ((int64_t)topk + window > (1 << 24)) return HS2_ERR_UNSUPPORTED;
+  EvictParams p;
+  const bool fp8 = dt == HS2_KV_FP8_E4M3;
+  p.c = paged_params(cache, B, kv_heads, dt);
+  p.dst_table = dst_table == cache->page_table ? nullptr : dst_table;
+  p.kept = kept;
+  p.new_len = new_len;
+  p.dst_max_pages = dst_max_pages;
+  p.topk = topk;
+  p.window = window;
+  p.row_bytes = kv_heads * D * (fp8 ? 1 : 2);
+  int cs = kEvMaxCluster;
+  while (cs > 1 && B * cs > 2 * sm_count()) cs /= 2;
+  p.cs = cs;
+  const int64_t run = (((reach + cs * kEvWarps - 1) / (cs * kEvWarps)) + 31) & ~31;
+  p.cache_keys = (int)std::min<int64_t>(kEvCache, run * kEvWarps);
+  const size_t bytes = sizeof(EvSmem) + (size_t)p.cache_keys * 4;
+  auto k = fp8 ? paged_evict_kernel<true> : paged_evict_kernel<false>;
+  if (!set_smem(k, (int)bytes)) return HS2_ERR_CUDA;
+  return launch(k, dim3((unsigned)(B * cs)), dim3(kEvThreads), bytes, (cudaStream_t)stream, cs, p);
+}
+
+}  // extern "C"

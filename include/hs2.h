@@ -441,6 +441,19 @@ HS2_API hs2_status hs2_add_rmsnorm(const void* X, const void* R, const void* gam
                                    float* Yq_scale, hs2_stream_t stream);
 
 /*
+ * hs2_fp8_gemm -- E4M3 matrix product with fp32 scales per block of 128:
+ *   C[m][n] = sum_kb A_scale[m][kb] * B_scale[n / 128][kb]
+ *                    * sum_{k in 128 kb .. 128 kb + 127} A[m][k] * B[n][k]
+ * summed in fp32, C bf16 [M][N] (round to nearest even).  A: E4M3 [M][K] (the
+ * output of hs2_add_rmsnorm, for example), A_scale fp32 [M][ceil(K / 128)];
+ * B: E4M3 [N][K] (nn.Linear weight layout), B_scale fp32 [ceil(N / 128)]
+ * [ceil(K / 128)].  Last blocks may be short.  K % 16 == 0; any M, N >= 1.  The
+ * result of a row does not depend on the run, only on M, N, K and the inputs.
+ */
+HS2_API hs2_status hs2_fp8_gemm(const void* A, const float* A_scale, int64_t M, const void* B,
+                                const float* B_scale, int N, int K, void* C, hs2_stream_t stream);
+
+/*
  * hs2_paged_append -- the new tokens' K and V rows to their pages.
  * Sequence b's new tokens are rows row_start[b] .. row_start[b+1]-1 (int32
  * [B + 1], device, ascending; rows outside row_start[0] .. row_start[B]-1 are

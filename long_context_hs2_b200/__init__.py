@@ -28,7 +28,7 @@ EXPORTED = ("hs2_bridge_kv", "hs2_full_attn_select_workspace", "hs2_full_attn_se
             "hs2_status_string", "hs2_version", "hs2_set_stage_events",
             "hs2_set_fault_injection", "hs2_full_attn_select_blocks", "hs2_cp_workspace",
             "hs2_cp_attn_partial", "hs2_cp_lse_combine", "hs2_cp_rescale", "hs2_cp_select_local",
-            "hs2_cp_merge_select", "hs2_set_phase_stamps", "hs2_add_rmsnorm",
+            "hs2_cp_merge_select", "hs2_set_phase_stamps", "hs2_add_rmsnorm", "hs2_fp8_gemm",
             "hs2_paged_append", "hs2_paged_attn", "hs2_paged_attn_workspace", "hs2_paged_evict")
 
 # Global-timer stamps per CTA written by the fused full-attention kernel when enabled.
@@ -114,6 +114,8 @@ def load_library(path: str = LIB_PATH):
     PC = ctypes.POINTER(hs2_paged_cache)
     lib.hs2_add_rmsnorm.restype = i32
     lib.hs2_add_rmsnorm.argtypes = [P, P, P, i64, i32, ctypes.c_float, P, P, P, P, P]
+    lib.hs2_fp8_gemm.restype = i32
+    lib.hs2_fp8_gemm.argtypes = [P, P, i64, P, P, i32, i32, P, P]
     lib.hs2_paged_append.restype = i32
     lib.hs2_paged_append.argtypes = [P, P, i64, i64, P, PC, i32, i32, i32, i32, P]
     lib.hs2_paged_attn_workspace.restype = sz
@@ -348,6 +350,16 @@ def hs2_add_rmsnorm(X, R, gamma, T, hidden, eps, sum=None, Y=None, Yq=None, Yq_s
                                      (Yq_scale, 4, T * ((hidden + 127) // 128), True)))
     _check("hs2_add_rmsnorm", load_library().hs2_add_rmsnorm(
         p[0], p[1], p[2], T, hidden, eps, p[3], p[4], p[5], p[6], _stream(stream)))
+
+
+def hs2_fp8_gemm(A, A_scale, M, B, B_scale, N, K, C, stream=None):
+    """C = A B^T in E4M3 with a scale per 1 x 128 of A and 128 x 128 of B; C bf16 [M, N]."""
+    kb = (K + 127) // 128
+    p = _tensors("hs2_fp8_gemm", ((A, 1, M * K, True), (A_scale, 4, M * kb, True),
+                                  (B, 1, N * K, True),
+                                  (B_scale, 4, (N + 127) // 128 * kb, True), (C, 2, M * N, True)))
+    _check("hs2_fp8_gemm", load_library().hs2_fp8_gemm(p[0], p[1], M, p[2], p[3], N, K, p[4],
+                                                       _stream(stream)))
 
 
 def hs2_paged_append(K, V, ld, n_rows, row_start, cache: hs2_paged_cache, B, kv_heads, D, dt,

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "add_rmsnorm.cuh"
+#include "fp8_gemm.cuh"
 #include "paged_attn.cuh"
 #include "paged_cache.cuh"
 #include "paged_evict.cuh"
@@ -104,9 +105,72 @@ hs2_status run_paged_attn(const CUtensorMap& km, const CUtensorMap& vm, const Pa
   return launch_ex(kw, dim3(p.grid), dim3(kPaThreads), SW::kBytes, s, 1, false, true, km, p);
 }
 
+// ------------------------------------------------------------- E4M3 product --
+template <int BN, int CW>
+hs2_status run_fp8_gemm(const void* A, const void* B, Fp8GemmParams p, cudaStream_t s) {
+  using SM = FgSmem<BN, CW>;
+  CUtensorMap am, bm;
+  if (!make_map_2d(&am, A, (uint64_t)p.M, (uint64_t)p.K, 1, kFgBK, 128) ||
+      !make_map_2d(&bm, B, (uint64_t)p.N, (uint64_t)p.K, 1, kFgBK, BN))
+    return HS2_ERR_CUDA;
+  p.m_tiles = (p.M + 127) / 128;
+  p.n_tiles = (p.N + BN - 1) / BN;
+  auto k = fp8_gemm_kernel<BN, CW>;
+  if (!set_smem(k, SM::kBytes)) return HS2_ERR_CUDA;
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+  if (tiles > INT32_MAX) return HS2_ERR_UNSUPPORTED;
+  return launch(k, dim3((unsigned)std::min<int64_t>(tiles, sm_count())), dim3(SM::kThreads),
+                SM::kBytes, s, 1, am, bm, p);
+}
+
+template <int NP>
+hs2_status run_fp8_gemm_small(const void* A, const void* B, Fp8GemmParams p, cudaStream_t s) {
+  using SM = FsSmem<NP>;
+  CUtensorMap am, bm;
+  if (!make_map_2d(&am, A, (uint64_t)p.M, (uint64_t)p.K, 1, kFgBK, NP) ||
+      !make_map_2d(&bm, B, (uint64_t)p.N, (uint64_t)p.K, 1, kFgBK, 128))
+    return HS2_ERR_CUDA;
+  p.m_tiles = (p.M + NP - 1) / NP;
+  p.n_tiles = (p.N + 127) / 128;
+  const int64_t segs = (int64_t)p.m_tiles * p.n_tiles;
+  int cs = kFsMaxCluster;
+  while (cs > 1 && (segs * cs > sm_count() || cs > p.kb)) cs /= 2;
+  auto k = fp8_gemm_small_kernel<NP>;
+  if (!set_smem(k, SM::kBytes)) return HS2_ERR_CUDA;
+  if (segs * cs > INT32_MAX) return HS2_ERR_UNSUPPORTED;
+  return launch(k, dim3((unsigned)(segs * cs)), dim3(kFsThreads), SM::kBytes, s, cs, am, bm, p,
+                cs);
+}
+
 }  // namespace
 
 extern "C" {
+
+hs2_status hs2_fp8_gemm(const void* A, const float* A_scale, int64_t M, const void* B,
+                        const float* B_scale, int N, int K, void* C, hs2_stream_t stream) {
+  if (!A || !A_scale || !B || !B_scale || !C || M < 1 || N < 1 || K < 1) return HS2_ERR_INVALID_ARG;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(C) || !aligned4(A_scale) || !aligned4(B_scale))
+    return HS2_ERR_INVALID_ARG;
+  if (K % 16 != 0 || M > INT32_MAX - 128 || N > INT32_MAX - 256 || K > INT32_MAX - 128)
+    return HS2_ERR_UNSUPPORTED;
+  Fp8GemmParams p;
+  p.sa = A_scale;
+  p.sb = B_scale;
+  p.c = static_cast<__nv_bfloat16*>(C);
+  p.M = (int)M;
+  p.N = N;
+  p.K = K;
+  p.kb = (K + kFgBK - 1) / kFgBK;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (M <= 16) return run_fp8_gemm_small<16>(A, B, p, s);
+  if (M <= 32) return run_fp8_gemm_small<32>(A, B, p, s);
+  if (M <= 64) return run_fp8_gemm_small<64>(A, B, p, s);
+  if (M <= 128) return run_fp8_gemm_small<128>(A, B, p, s);
+  const int64_t mt = (M + 127) / 128;
+  if (mt * ((N + 255) / 256) >= sm_count()) return run_fp8_gemm<256, 8>(A, B, p, s);
+  if (mt * ((N + 127) / 128) >= sm_count() / 2) return run_fp8_gemm<128, 8>(A, B, p, s);
+  return run_fp8_gemm<64, 8>(A, B, p, s);
+}
 
 hs2_status hs2_add_rmsnorm(const void* X, const void* R, const void* gamma, int64_t T, int hidden,
                            float eps, void* sum, void* Y, void* Yq, float* Yq_scale,

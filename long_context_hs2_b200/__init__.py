@@ -140,6 +140,9 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle without a Stream object
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -299,13 +302,15 @@ def hs2_cp_merge_select(cand_score, cand_idx, G, B, T, q_pos0, topk, window, idx
 def _tensors(fn: str, specs):
     """Device pointers of (tensor, element size, least elements, contiguous) entries."""
     import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    out = []
+    dev, out = None, []
     for t, size, least, contiguous in specs:
         if t is None or isinstance(t, int):
             out.append(t)
             continue
-        if (t.get_device() != dev or t.element_size() != size or t.numel() < least
+        d = t.get_device()
+        if dev is None and d >= 0:
+            dev = torch.cuda.current_device()
+        if (d != dev or t.element_size() != size or t.numel() < least
                 or (contiguous and not t.is_contiguous())):
             raise Hs2Error(fn, 1)
         out.append(t.data_ptr())

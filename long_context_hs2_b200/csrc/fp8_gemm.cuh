@@ -34,6 +34,7 @@ struct Fp8GemmParams {
   __nv_bfloat16* c;
   int M, N, K, kb;                     // kb = ceil(K / 128)
   int m_tiles, n_tiles;
+  int sa_vec;                          // rows of sa start on 16 bytes
 };
 
 // kind::f8f6f4, A = B = E4M3, fp32 accumulator, both K-major.
@@ -65,13 +66,16 @@ struct FgSmem {
   static constexpr int kTmem = 2 * BN < 32 ? 32 : 2 * BN;
 };
 
-// Registers moved between the warpgroups of a block launched with 168 per
-// thread: 128 * 40 + 256 * 232 = 384 * 168, the whole of what it was given.
-__device__ __forceinline__ void regs_give_up() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-}
-__device__ __forceinline__ void regs_take() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+// Scales of blocks kb .. kb + 3 of a row (those below n).
+__device__ __forceinline__ void load_scales4(const float* row, int kb, int n, int vec, float* s) {
+  if (vec && kb + 4 <= n) {
+    const float4 v = *reinterpret_cast<const float4*>(row + kb);
+    s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (kb + i < n) s[i] = row[kb + i];
+  }
 }
 
 template <int BN, int CW>
@@ -112,14 +116,11 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
   const uint32_t tmem = *tmem_slot;
   constexpr bool kMove = COLS >= 128;   // 128 sums a thread do not fit 168 registers
   static_assert(!kMove || CW == 8, "the registers' split is for 12 warps");
-  if (kMove) {
-    if (warp < 4) regs_give_up();
-    else regs_take();
-  }
 
-  if (warp == 0) {
-    // ------------------------------------------------------ TMA producer
-    if (lane == 0) {
+  if (warp < 4) {
+    if (kMove) regs_give_up();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------- TMA producer
       tma_prefetch_desc(&amap);
       tma_prefetch_desc(&bmap);
       const uint64_t pol = policy_evict_normal();
@@ -136,34 +137,42 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
           tma_load_2d(a + SM::kABytes, &bmap, &full[s], kb * kFgBK, n0, pol);
         }
       }
-    }
-  } else if (warp == 1) {
-    // -------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = tc_idesc_e4m3(128, BN);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        for (int kb = 0; kb < p.kb; ++kb, ++it) {
-          const int s = it % SM::kStages, acc = it & 1;
-          if (!mbar_wait(&acc_empty[acc], ((it >> 1) & 1) ^ 1) ||
-              !mbar_wait(&full[s], (it / SM::kStages) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t addr = smem_u32(smem + s * SM::kStage);
-          const uint64_t ad = sw128_kmajor_desc(addr), bd = sw128_kmajor_desc(addr + SM::kABytes);
+    } else if (warp == 1) {
+      // ------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc = tc_idesc_e4m3(128, BN);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+          for (int kb = 0; kb < p.kb; ++kb, ++it) {
+            const int s = it % SM::kStages, acc = it & 1;
+            if (!mbar_wait(&acc_empty[acc], ((it >> 1) & 1) ^ 1) ||
+                !mbar_wait(&full[s], (it / SM::kStages) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t addr = smem_u32(smem + s * SM::kStage);
+            const uint64_t ad = sw128_kmajor_desc(addr),
+                           bd = sw128_kmajor_desc(addr + SM::kABytes);
 #pragma unroll
-          for (int k = 0; k < kFgBK / 32; ++k)   // +32 bytes along K per step
-            tc_mma_f8(tmem + acc * BN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
-          tc_commit(&empty[s]);
-          tc_commit(&acc_full[acc]);
+            for (int k = 0; k < kFgBK / 32; ++k)   // +32 bytes along K per step
+              tc_mma_f8(tmem + acc * BN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+            tc_commit(&empty[s]);
+            tc_commit(&acc_full[acc]);
+          }
         }
+        // the accumulators are read before tensor memory is given back
+        for (uint32_t i = it >= 2 ? it - 2 : 0; i < it && ok; ++i)
+          ok = mbar_wait(&acc_empty[i & 1], (i >> 1) & 1);
       }
+      __syncwarp();
+      tc_fence_after();
+      tmem_dealloc(tmem, SM::kTmem);
     }
-  } else if (warp >= 4) {
+  } else {
     // --------------------------------------------------------- consumers
+    if (kMove) regs_take();
     const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + part * COLS;
     uint32_t it = 0;
@@ -172,30 +181,43 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
       const int m = tile / p.n_tiles * 128 + quarter * 32 + lane;
       const int n0 = tile % p.n_tiles * BN + part * COLS;
       const float* sa = p.sa + (size_t)min(m, p.M - 1) * p.kb;
-      // one or two blocks of 128 columns (the last column's block may not exist)
-      const int nb_last = (p.N - 1) / 128;
-      const float* sb0 = p.sb + (size_t)min(n0 / 128, nb_last) * p.kb;
+      const float* sb = p.sb + (size_t)min(n0 / 128, (p.N - 1) / 128) * p.kb;
       float acc[COLS];
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.f;
-      float s_next = sa[0] * sb0[0];
+      // scales are loaded a group of four blocks ahead: a row's lie together, so
+      // one 16-byte load (where the rows are aligned) serves four blocks, and no
+      // load is waited for where it is issued
+      float cur[4], nxt[4];
+      load_scales4(sa, 0, p.kb, p.sa_vec, nxt);
+      float sb_next = sb[0];
       for (int kb = 0; kb < p.kb; ++kb, ++it) {
-        const float s = s_next;
-        if (kb + 1 < p.kb) s_next = sa[kb + 1] * sb0[kb + 1];
+        if ((kb & 3) == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+          load_scales4(sa, kb + 4, p.kb, p.sa_vec, nxt);
+        }
+        const float s = (kb & 2 ? (kb & 1 ? cur[3] : cur[2]) : (kb & 1 ? cur[1] : cur[0])) * sb_next;
+        if (kb + 1 < p.kb) sb_next = sb[kb + 1];
         const int a = it & 1;
         if (!mbar_wait(&acc_full[a], (it >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
+        // a chunk of columns is read while the one before it is added
+        float v[2][32];
+        tmem_ld32(taddr + a * BN, v[0]);
 #pragma unroll
-        for (int c = 0; c < COLS; c += 32) {
-          float v[32];
-          tmem_ld32(taddr + a * BN + c, v);
+        for (int c = 0; c < COLS / 32; ++c) {
           tmem_ld_wait();
+          if (c + 1 < COLS / 32) {
+            tmem_ld32(taddr + a * BN + (c + 1) * 32, v[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[a]);
+          }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(v[i], s, acc[c + i]);
+          for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[c & 1][i], s, acc[c * 32 + i]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[a]);
       }
       if (ok && m < p.M) {
         __nv_bfloat16* out = p.c + (size_t)m * p.N + n0;
@@ -212,11 +234,6 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
         }
       }
     }
-  }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, SM::kTmem);
   }
 }
 

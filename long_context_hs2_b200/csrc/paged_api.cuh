@@ -96,7 +96,8 @@ hs2_status run_paged_attn(const CUtensorMap& km, const CUtensorMap& vm, const Pa
   auto k = paged_attn_kernel<MT, D, FP8>;
   auto kw = paged_weight_kernel<MT, D, FP8>;
   if (!set_smem(k, SM::kBytes)) return HS2_ERR_CUDA;
-  hs2_status st = launch(k, dim3(p.grid), dim3(kPaThreads), SM::kBytes, s, 1, km, vm, p);
+  hs2_status st = launch(k, dim3(p.grid), dim3(kPaAttnThreads<MT, D>), SM::kBytes, s, 1, km, vm,
+                         p);
   if (st != HS2_OK) return st;
   st = launch_ex(paged_attn_combine_kernel<D>, dim3((unsigned)(p.c.B * p.H)), dim3(D), 0, s, 1,
                  false, true, p);
@@ -161,6 +162,7 @@ hs2_status hs2_fp8_gemm(const void* A, const float* A_scale, int64_t M, const vo
   p.N = N;
   p.K = K;
   p.kb = (K + kFgBK - 1) / kFgBK;
+  p.sa_vec = p.kb % 4 == 0 && aligned16(A_scale);
   cudaStream_t s = (cudaStream_t)stream;
   if (M <= 16) return run_fp8_gemm_small<16>(A, B, p, s);
   if (M <= 32) return run_fp8_gemm_small<32>(A, B, p, s);

@@ -44,6 +44,13 @@ namespace hs2 {
 constexpr int kPaTile = 128;                 // positions per tile
 constexpr int kPaWarps = 8;                  // consumer warps, 16 positions each
 constexpr int kPaThreads = 32 * (kPaWarps + 1);
+// 32 rows x 128 columns of O per warp are 128 registers a thread: the producer's
+// warpgroup is made whole and gives its registers to the consumers
+// (128 * 40 + 256 * 232 = 384 * 168, all that the block was launched with).
+template <int MT, int D>
+constexpr bool kPaMove = MT == 2 && D == 128;
+template <int MT, int D>
+constexpr int kPaAttnThreads = kPaMove<MT, D> ? 32 * (kPaWarps + 4) : kPaThreads;
 constexpr float kPaSlack = 8.f;              // log2 a logit may exceed its reference by
 constexpr float kPaMinScale = 1e-30f;        // least reference of v_scale (its inverse is finite)
 constexpr float kPaLog2e = 1.4426950408889634f;
@@ -411,7 +418,7 @@ __device__ __forceinline__ void pa_scores(uint32_t qs, uint32_t kt, int key0,
 }
 
 template <int MT, int D, bool FP8>
-__global__ void __launch_bounds__(kPaThreads, 1)
+__global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
                       const PagedAttnParams p) {
   using SM = PaSmem<MT, D, FP8, false>;
@@ -454,8 +461,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   PaWalk w;
   w.start(p.c, p.c.heads, (int)work[3], work[2], work[0], work[1]);
 
-  if (warp == kPaWarps) {
+  if (warp >= kPaWarps) {
     // ---------------------------------------------------------- producer
+    if (kPaMove<MT, D>) {
+      regs_give_up();
+      if (warp > kPaWarps) return;
+    }
     const uint64_t kpol = policy_evict_normal(), vpol = policy_evict_first();
     uint32_t it = 0;
     bool ok = true;
@@ -482,6 +493,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   }
 
   // ------------------------------------------------------------ consumers
+  if (kPaMove<MT, D>) regs_take();
   uint8_t* qs = smem + SM::kQOff;
   float2* ml = reinterpret_cast<float2*>(smem + SM::kMlOff);
   float* row_scale = reinterpret_cast<float*>(smem + SM::kRowOff);

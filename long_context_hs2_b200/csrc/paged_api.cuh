@@ -6,6 +6,7 @@
 #include "add_rmsnorm.cuh"
 #include "fp8_gemm.cuh"
 #include "paged_attn.cuh"
+#include "paged_attn_tc.cuh"
 #include "paged_cache.cuh"
 #include "paged_evict.cuh"
 
@@ -93,11 +94,18 @@ hs2_status run_paged_attn(const CUtensorMap& km, const CUtensorMap& vm, const Pa
                           bool weight, cudaStream_t s) {
   using SM = PaSmem<MT, D, FP8, false>;
   using SW = PaSmem<MT, D, FP8, true>;
-  auto k = paged_attn_kernel<MT, D, FP8>;
   auto kw = paged_weight_kernel<MT, D, FP8>;
-  if (!set_smem(k, SM::kBytes)) return HS2_ERR_CUDA;
-  hs2_status st = launch(k, dim3(p.grid), dim3(kPaAttnThreads<MT, D>), SM::kBytes, s, 1, km, vm,
-                         p);
+  hs2_status st;
+  if (D == 128 && p.c.page_shift >= 3) {
+    using ST = PtSmem<16 * MT, FP8>;
+    auto k = paged_attn_tc_kernel<16 * MT, FP8>;
+    if (!set_smem(k, ST::kBytes)) return HS2_ERR_CUDA;
+    st = launch(k, dim3(p.grid), dim3(kPtThreads), ST::kBytes, s, 1, km, vm, p);
+  } else {
+    auto k = paged_attn_kernel<MT, D, FP8>;
+    if (!set_smem(k, SM::kBytes)) return HS2_ERR_CUDA;
+    st = launch(k, dim3(p.grid), dim3(kPaAttnThreads<MT, D>), SM::kBytes, s, 1, km, vm, p);
+  }
   if (st != HS2_OK) return st;
   st = launch_ex(paged_attn_combine_kernel<D>, dim3((unsigned)(p.c.B * p.H)), dim3(D), 0, s, 1,
                  false, true, p);

@@ -483,7 +483,8 @@ HS2_API size_t hs2_paged_attn_workspace(int B, int H, int kv_heads, int D);
  *   accumulate: weight_j += sum_h exp(s_hj - lse_h)  (all H heads)
  * Q, O: bf16 [B][H][D]; lse: fp32 [B][H] or NULL.  seq_len[b] == 0: O = 0, lse =
  * -inf.  accumulate needs cache->weight, and pages that no two sequences share
- * (shared pages are fine without it).  H % kv_heads == 0, H / kv_heads <= 32.
+ * (shared pages are fine without it).  H % kv_heads == 0, H / kv_heads <= 32, and
+ * B * kv_heads * max_pages * page_size / 128 < 2^31 - 1024.
  * The workspace needs no initial value and is free again when the call's work
  * is done.
  */

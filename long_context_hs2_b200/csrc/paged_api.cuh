@@ -100,7 +100,7 @@ hs2_status run_paged_attn(const CUtensorMap& km, const CUtensorMap& vm, const Pa
     using ST = PtSmem<16 * MT, FP8>;
     auto k = paged_attn_tc_kernel<16 * MT, FP8>;
     if (!set_smem(k, ST::kBytes)) return HS2_ERR_CUDA;
-    st = launch(k, dim3(p.grid), dim3(kPtThreads), ST::kBytes, s, 1, km, vm, p);
+    st = launch(k, dim3(p.grid), dim3(ST::kThreads), ST::kBytes, s, 1, km, vm, p);
   } else {
     auto k = paged_attn_kernel<MT, D, FP8>;
     if (!set_smem(k, SM::kBytes)) return HS2_ERR_CUDA;
@@ -264,7 +264,10 @@ hs2_status hs2_paged_attn(const void* Q, const hs2_paged_cache* cache, int B, in
   hs2_status st = check_paged(cache, B, kv_heads, D, dt);
   if (st != HS2_OK) return st;
   if (!check_heads(H, kv_heads) || (accumulate && !cache->weight)) return HS2_ERR_INVALID_ARG;
-  if (H / kv_heads > 32 || (int64_t)B * H > INT32_MAX) return HS2_ERR_UNSUPPORTED;
+  // tiles and shares are counted in 31 bits
+  const int64_t tiles = ((int64_t)cache->max_pages * cache->page_size + kPaTile - 1) / kPaTile;
+  if (H / kv_heads > 32 || (int64_t)B * H > INT32_MAX || tiles * B * kv_heads > INT32_MAX - 1024)
+    return HS2_ERR_UNSUPPORTED;
   const PagedPlan pl = paged_plan(B, H, kv_heads, D);
   if (!workspace || !aligned16(workspace) || workspace_bytes < pl.total)
     return HS2_ERR_WORKSPACE;

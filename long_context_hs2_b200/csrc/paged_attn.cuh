@@ -68,37 +68,36 @@ struct PagedAttnParams {
   float scale_log2;
 };
 
-// Shares of `total` tiles over the CTAs that have any.
+// Shares of `total` tiles: CTA c has tiles [c * chunk, (c + 1) * chunk) of them.
 struct PaShare {
-  long long total, n;
-  __device__ __forceinline__ long long begin(long long c) const { return c * total / n; }
-  // the CTA whose share holds tile g
-  __device__ __forceinline__ long long owner(long long g) const {
-    return ((g + 1) * n + total - 1) / total - 1;
-  }
+  int total, chunk;
+  __device__ __forceinline__ PaShare(int total_, int grid)
+      : total(total_), chunk(max(1, (total_ + grid - 1) / grid)) {}
+  __device__ __forceinline__ int begin(int c) const { return (int)min((long long)total, (long long)c * chunk); }
+  __device__ __forceinline__ int owner(int g) const { return g / chunk; }
 };
 __device__ __forceinline__ int pa_tiles(int len) { return (len + kPaTile - 1) / kPaTile; }
 
 // One warp: all tiles of the call, `mult` items per sequence.
-__device__ __forceinline__ long long pa_total(const PagedCache& c, int mult) {
-  long long n = 0;
+__device__ __forceinline__ int pa_total(const PagedCache& c, int mult) {
+  int n = 0;
   for (int b = threadIdx.x & 31; b < c.B; b += 32) n += pa_tiles(paged_len(c, b));
 #pragma unroll
   for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n * mult;
 }
 // One warp: the sequence that holds tile g, and the first tile of that sequence.
-__device__ __forceinline__ void pa_find(const PagedCache& c, int mult, long long g, int& b_out,
-                                        long long& first) {
+__device__ __forceinline__ void pa_find(const PagedCache& c, int mult, int g, int& b_out,
+                                        int& first) {
   const int lane = threadIdx.x & 31;
-  long long base = 0;
+  int base = 0;
   for (int b0 = 0; b0 < c.B; b0 += 32) {
     const int b = b0 + lane;
-    const long long mine = b < c.B ? (long long)pa_tiles(paged_len(c, b)) * mult : 0;
-    long long inc = mine;
+    const int mine = b < c.B ? pa_tiles(paged_len(c, b)) * mult : 0;
+    int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, g < base + inc);
@@ -114,20 +113,29 @@ __device__ __forceinline__ void pa_find(const PagedCache& c, int mult, long long
   first = base;
 }
 
+// One warp: the CTA's share, for PaWalk::start (empty: x == y).
+__device__ __forceinline__ int4 pa_share(const PagedCache& c, int mult, int grid) {
+  const PaShare sh(pa_total(c, mult), grid);
+  int4 w = make_int4(sh.begin(blockIdx.x), sh.begin(blockIdx.x + 1), 0, 0);
+  if (w.x < w.y) pa_find(c, mult, w.x, w.w, w.z);
+  return w;
+}
+
 // Walks a CTA's share item by item.
 struct PaWalk {
   int b, head, len, nt, t0, t1;   // the current segment: tiles [t0, t1) of nt
-  long long g, end;               // next tile of the share, and its end
-  __device__ __forceinline__ void start(const PagedCache& c, int mult, int b0, long long first,
-                                        long long g0, long long g1) {
+  int g, end;                     // next tile of the share, and its end
+  // the CTA's share: {first tile, end, first tile of the first sequence, that sequence}
+  __device__ __forceinline__ void start(const PagedCache& c, const int4 work) {
+    const int g0 = work.x, g1 = work.y, first = work.z, b0 = work.w;
     b = b0;
     g = g0;
     end = g1;
     len = paged_len(c, b);
     nt = pa_tiles(len);
-    head = (int)((g0 - first) / nt);
-    t0 = (int)((g0 - first) - (long long)head * nt);
-    t1 = (int)min((long long)nt, t0 + (end - g));
+    head = (g0 - first) / nt;
+    t0 = (g0 - first) - head * nt;
+    t1 = min(nt, t0 + (end - g));
   }
   // to the next segment; false at the share's end
   __device__ __forceinline__ bool next(const PagedCache& c, int mult) {
@@ -142,7 +150,7 @@ struct PaWalk {
         nt = pa_tiles(len);
       } while (nt == 0);
     }
-    t1 = (int)min((long long)nt, end - g);
+    t1 = min(nt, end - g);
     return true;
   }
 };
@@ -164,7 +172,7 @@ struct PaSmem {
   static constexpr int kMlOff = kQOff + kQBytes;             // float2 [warps][MT * 16]
   static constexpr int kRowOff = kMlOff + kPaWarps * MT * 16 * 8;   // float [MT * 16]
   static constexpr int kBarOff = kRowOff + MT * 16 * 4;
-  static constexpr int kWorkOff = kBarOff + 2 * 8 * 8;       // long long [4]
+  static constexpr int kWorkOff = kBarOff + 2 * 8 * 8;       // int4
   static constexpr int kBytes = kWorkOff + 64 + 1024;
   // columns of the output joined at a time in a stage's bytes
   static constexpr int kJoin0 = kKvBytes / (kPaWarps * MT * 16 * 4);
@@ -423,11 +431,13 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
                       const PagedAttnParams p) {
   using SM = PaSmem<MT, D, FP8, false>;
   static_assert(SM::kBytes <= 232448 && SM::kStages >= 2, "shared memory per CTA");
+  static_assert(SM::kWorkOff % 16 == 0 && SM::kBarOff % 8 == 0 && SM::kMetaBytes % 16 == 0,
+                "alignment of shared words");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
   uint64_t* empty = full + 8;
-  long long* work = reinterpret_cast<long long*>(smem + SM::kWorkOff);
+  int4* work = reinterpret_cast<int4*>(smem + SM::kWorkOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool small = p.c.page_shift < 3;
 
@@ -440,26 +450,13 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
     fence_mbar_init();
   }
   if (warp == kPaWarps) {
-    const long long total = pa_total(p.c, p.c.heads);
-    PaShare sh{total, min((long long)p.grid, total)};
-    long long g0 = 0, g1 = 0, first = 0;
-    int b = 0;
-    if (blockIdx.x < sh.n) {
-      g0 = sh.begin(blockIdx.x);
-      g1 = sh.begin(blockIdx.x + 1);
-      pa_find(p.c, p.c.heads, g0, b, first);
-    }
-    if (lane == 0) {
-      work[0] = g0;
-      work[1] = g1;
-      work[2] = first;
-      work[3] = b;
-    }
+    const int4 mine = pa_share(p.c, p.c.heads, p.grid);
+    if (lane == 0) *work = mine;
   }
   __syncthreads();
-  if (work[0] == work[1]) return;
+  if (work->x == work->y) return;
   PaWalk w;
-  w.start(p.c, p.c.heads, (int)work[3], work[2], work[0], work[1]);
+  w.start(p.c, *work);
 
   if (warp >= kPaWarps) {
     // ---------------------------------------------------------- producer
@@ -779,28 +776,23 @@ constexpr int kPaMaxParts = 512;   // grid CTAs at most
 template <int D>
 __global__ void __launch_bounds__(D) paged_attn_combine_kernel(const PagedAttnParams p) {
   __shared__ float wgt[kPaMaxParts];
-  __shared__ long long info[3];
+  __shared__ int info[3];
   __shared__ float red[2];
   const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, head = h / p.G, r = h % p.G;
   const size_t row = (size_t)b * p.H + h;
   pdl_launch_dependents();
   if (threadIdx.x < 32) {
-    long long before = 0, total = 0;
+    int before = 0, total = 0;
     for (int i = threadIdx.x; i < p.c.B; i += 32) {
       const int n = pa_tiles(paged_len(p.c, i));
       total += n;
       if (i < b) before += n;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    before = __reduce_add_sync(0xffffffffu, before);
     if (threadIdx.x == 0) {
-      const int nt = pa_tiles(paged_len(p.c, b));
-      total *= p.c.heads;
-      const long long g = before * p.c.heads + (long long)head * nt;
-      PaShare sh{total, min((long long)p.grid, total)};
+      const int nt = pa_tiles(paged_len(p.c, b)), g = before * p.c.heads + head * nt;
+      const PaShare sh(total * p.c.heads, p.grid);
       info[0] = nt ? sh.owner(g) : 0;
       info[1] = nt ? sh.owner(g + nt - 1) : 0;
       info[2] = nt;
@@ -808,7 +800,7 @@ __global__ void __launch_bounds__(D) paged_attn_combine_kernel(const PagedAttnPa
   }
   __syncthreads();
   pdl_wait();
-  const int c0 = (int)info[0], c1 = (int)info[1];
+  const int c0 = info[0], c1 = info[1];
   if (info[2] == 0) {
     p.o[row * D + threadIdx.x] = __float2bfloat16_rn(0.f);
     if (threadIdx.x == 0) {
@@ -862,11 +854,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     paged_weight_kernel(const __grid_constant__ CUtensorMap km, const PagedAttnParams p) {
   using SM = PaSmem<MT, D, FP8, true>;
   static_assert(SM::kBytes <= 232448 && SM::kStages >= 2, "shared memory per CTA");
+  static_assert(SM::kWorkOff % 16 == 0 && SM::kBarOff % 8 == 0 && SM::kMetaBytes % 16 == 0,
+                "alignment of shared words");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
   uint64_t* empty = full + 8;
-  long long* work = reinterpret_cast<long long*>(smem + SM::kWorkOff);
+  int4* work = reinterpret_cast<int4*>(smem + SM::kWorkOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool small = p.c.page_shift < 3;
   if (threadIdx.x == 0) {
@@ -877,28 +871,15 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     fence_mbar_init();
   }
   if (warp == kPaWarps) {
-    const long long total = pa_total(p.c, 1);
-    PaShare sh{total, min((long long)p.grid, total)};
-    long long g0 = 0, g1 = 0, first = 0;
-    int b = 0;
-    if (blockIdx.x < sh.n) {
-      g0 = sh.begin(blockIdx.x);
-      g1 = sh.begin(blockIdx.x + 1);
-      pa_find(p.c, 1, g0, b, first);
-    }
-    if (lane == 0) {
-      work[0] = g0;
-      work[1] = g1;
-      work[2] = first;
-      work[3] = b;
-    }
+    const int4 mine = pa_share(p.c, 1, p.grid);
+    if (lane == 0) *work = mine;
   }
   __syncthreads();
   pdl_wait();
-  if (work[0] == work[1]) return;
+  if (work->x == work->y) return;
   // a segment's tiles are walked once per K/V head inside each tile
   PaWalk w;
-  w.start(p.c, 1, (int)work[3], work[2], work[0], work[1]);
+  w.start(p.c, *work);
 
   if (warp == kPaWarps) {
     const uint64_t kpol = policy_evict_normal();

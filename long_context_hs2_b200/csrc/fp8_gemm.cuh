@@ -115,10 +115,10 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   constexpr bool kMove = COLS >= 128;   // 128 sums a thread do not fit 168 registers
-  static_assert(!kMove || CW == 8, "the registers' split is for 12 warps");
+  static_assert(!kMove || CW == 8, "128 * 40 + 256 * 232 = 384 * 168, what the block is given");
 
   if (warp < 4) {
-    if (kMove) regs_give_up();
+    if (kMove) regs_give_up<40>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer
       tma_prefetch_desc(&amap);
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
     }
   } else {
     // --------------------------------------------------------- consumers
-    if (kMove) regs_take();
+    if (kMove) regs_take<232>();
     const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + part * COLS;
     uint32_t it = 0;

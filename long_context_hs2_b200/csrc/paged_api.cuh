@@ -107,6 +107,13 @@ hs2_status run_paged_attn(const CUtensorMap& km, const CUtensorMap& vm, const Pa
     st = launch(k, dim3(p.grid), dim3(kPaAttnThreads<MT, D>), SM::kBytes, s, 1, km, vm, p);
   }
   if (st != HS2_OK) return st;
+  if (weight && D == 128 && p.c.page_shift >= 3 && p.c.heads * 16 * MT <= kPwRows) {
+    // joins the parts as well
+    using SP = PwSmem<16 * MT, FP8>;
+    auto k = paged_weight_tc_kernel<16 * MT, FP8>;
+    if (!set_smem(k, SP::kBytes)) return HS2_ERR_CUDA;
+    return launch_ex(k, dim3(p.grid), dim3(SP::kThreads), SP::kBytes, s, 1, false, true, km, p);
+  }
   st = launch_ex(paged_attn_combine_kernel<D>, dim3((unsigned)(p.c.B * p.H)), dim3(D), 0, s, 1,
                  false, true, p);
   if (st != HS2_OK || !weight) return st;

@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
   if (warp >= kPaWarps) {
     // ---------------------------------------------------------- producer
     if (kPaMove<MT, D>) {
-      regs_give_up();
+      regs_give_up<40>();
       if (warp > kPaWarps) return;
     }
     const uint64_t kpol = policy_evict_normal(), vpol = policy_evict_first();
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
   }
 
   // ------------------------------------------------------------ consumers
-  if (kPaMove<MT, D>) regs_take();
+  if (kPaMove<MT, D>) regs_take<232>();
   uint8_t* qs = smem + SM::kQOff;
   float2* ml = reinterpret_cast<float2*>(smem + SM::kMlOff);
   float* row_scale = reinterpret_cast<float*>(smem + SM::kRowOff);
@@ -769,80 +769,125 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
 }
 
 // ----------------------------------------------------------------- combine --
-// One CTA of D threads per (sequence, head): joins the parts of an item that
-// was cut, in ascending order; empty sequences get O = 0, lse = -inf.
 constexpr int kPaMaxParts = 512;   // grid CTAs at most
 
-template <int D>
-__global__ void __launch_bounds__(D) paged_attn_combine_kernel(const PagedAttnParams p) {
-  __shared__ float wgt[kPaMaxParts];
-  __shared__ int info[3];
-  __shared__ float red[2];
-  const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, head = h / p.G, r = h % p.G;
-  const size_t row = (size_t)b * p.H + h;
-  pdl_launch_dependents();
-  if (threadIdx.x < 32) {
-    int before = 0, total = 0;
-    for (int i = threadIdx.x; i < p.c.B; i += 32) {
-      const int n = pa_tiles(paged_len(p.c, i));
-      total += n;
-      if (i < b) before += n;
-    }
-    total = __reduce_add_sync(0xffffffffu, total);
-    before = __reduce_add_sync(0xffffffffu, before);
-    if (threadIdx.x == 0) {
-      const int nt = pa_tiles(paged_len(p.c, b)), g = before * p.c.heads + head * nt;
-      const PaShare sh(total * p.c.heads, p.grid);
-      info[0] = nt ? sh.owner(g) : 0;
-      info[1] = nt ? sh.owner(g + nt - 1) : 0;
-      info[2] = nt;
-    }
+// Shared memory of joining a row.
+struct PaJoin {
+  float wgt[kPaMaxParts];
+  float top, sum;
+  int first, last, tiles, pad;
+};
+
+// One warp: which CTAs have a part of item (b, head), {first, last, tiles}: the
+// first one's share ends inside the item (its part 1), the others' begin inside
+// it (their part 0).
+__device__ __forceinline__ int3 pa_item_parts(const PagedAttnParams& p, int b, int head) {
+  int before = 0, total = 0, mine = 0;
+  for (int i = threadIdx.x & 31; i < p.c.B; i += 32) {
+    const int n = pa_tiles(paged_len(p.c, i));
+    total += n;
+    if (i < b) before += n;
+    if (i == b) mine = n;
   }
-  __syncthreads();
-  pdl_wait();
-  const int c0 = info[0], c1 = info[1];
-  if (info[2] == 0) {
-    p.o[row * D + threadIdx.x] = __float2bfloat16_rn(0.f);
-    if (threadIdx.x == 0) {
+  total = __reduce_add_sync(0xffffffffu, total);
+  before = __reduce_add_sync(0xffffffffu, before);
+  const int nt = __reduce_add_sync(0xffffffffu, mine), g = before * p.c.heads + head * nt;
+  const PaShare sh(total * p.c.heads, p.grid);
+  return nt ? make_int3(sh.owner(g), sh.owner(g + nt - 1), nt) : make_int3(0, 0, 0);
+}
+
+// One warp, after the attention kernel: log2-domain lse of the item's row `lane`
+// (lanes past G: unspecified).
+__device__ __forceinline__ float pa_item_lse(const PagedAttnParams& p, int b, int head,
+                                             int lane) {
+  const int3 parts = pa_item_parts(p, b, head);
+  if (lane >= p.G) return 0.f;
+  if (parts.x == parts.y)
+    return p.lse[(size_t)b * p.H + (size_t)head * p.G + lane] * kPaLog2e;
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
+  for (int c = parts.x; c <= parts.y; ++c) {
+    const float2 v = p.part_ml[(size_t)(c * 2 + (c == parts.x)) * p.G + lane];
+    const float m = fmaxf(top, v.x);
+    if (m != -INFINITY) sum = sum * fast_exp2(top - m) + v.y * fast_exp2(v.x - m);
+    top = m;
+  }
+  return top + log2f(sum);
+}
+
+// D threads: joins the parts of row (sequence, query head) in ascending order;
+// empty sequences get O = 0, lse = -inf; an item that one CTA had is finished.
+template <int D>
+__device__ __forceinline__ void pa_join_sync() {
+  asm volatile("bar.sync 6, %0;" ::"n"(D) : "memory");
+}
+template <int D>
+__device__ __forceinline__ void pa_join_row(const PagedAttnParams& p, int row, int tid,
+                                            PaJoin& s, bool wait) {
+  const int b = row / p.H, h = row % p.H, head = h / p.G, r = h % p.G;
+  if (tid < 32) {
+    const int3 parts = pa_item_parts(p, b, head);
+    if (tid == 0) {
+      s.first = parts.x;
+      s.last = parts.y;
+      s.tiles = parts.z;
+    }
+    __syncwarp();
+    if (wait) pdl_wait();   // (each thread that reads or writes results waits)
+    const int n = parts.y - parts.x + 1;
+    if (n > 1) {
+      float top = -INFINITY, sum = 0.f;
+      for (int i = tid; i < n; i += 32)
+        top = fmaxf(top, p.part_ml[(size_t)((parts.x + i) * 2 + (i == 0)) * p.G + r].x);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int i = tid; i < n; i += 32) {
+        const float2 v = p.part_ml[(size_t)((parts.x + i) * 2 + (i == 0)) * p.G + r];
+        const float e = v.x == -INFINITY ? 0.f : fast_exp2(v.x - top);
+        s.wgt[i] = e;
+        sum += v.y * e;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (tid == 0) {
+        s.top = top;
+        s.sum = sum;
+      }
+    }
+  } else if (wait) {
+    pdl_wait();
+  }
+  pa_join_sync<D>();
+  const int c0 = s.first, n = s.last - s.first + 1;
+  __nv_bfloat16* out = p.o + (size_t)row * D + tid;
+  if (s.tiles == 0) {
+    *out = __float2bfloat16_rn(0.f);
+    if (tid == 0) {
       p.lse[row] = -INFINITY;
       if (p.lse_out) p.lse_out[row] = -INFINITY;
     }
-    return;
-  }
-  if (c0 == c1) return;   // one CTA had the whole item and finished it
-  const int n = c1 - c0 + 1;
-  // the first CTA ends inside the item (its part 1), later ones begin inside it (part 0)
-  if (threadIdx.x < 32) {
-    float top = -INFINITY, sum = 0.f;
-    for (int i = threadIdx.x; i < n; i += 32)
-      top = fmaxf(top, p.part_ml[(size_t)((c0 + i) * 2 + (i == 0)) * p.G + r].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int i = threadIdx.x; i < n; i += 32) {
-      const float2 v = p.part_ml[(size_t)((c0 + i) * 2 + (i == 0)) * p.G + r];
-      const float e = v.x == -INFINITY ? 0.f : fast_exp2(v.x - top);
-      wgt[i] = e;
-      sum += v.y * e;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (threadIdx.x == 0) {
-      red[0] = top;
-      red[1] = sum;
-    }
-  }
-  __syncthreads();
-  float a = 0.f;
+  } else if (n > 1) {
+    float a = 0.f;
 #pragma unroll 8
-  for (int i = 0; i < n; ++i)
-    a += wgt[i] * p.part_o[((size_t)((c0 + i) * 2 + (i == 0)) * p.G + r) * D + threadIdx.x];
-  const float sum = red[1];
-  p.o[row * D + threadIdx.x] = __float2bfloat16_rn(sum == 0.f ? 0.f : a / sum);
-  if (threadIdx.x == 0) {
-    const float v = (red[0] + log2f(sum)) * kPaLn2;
-    p.lse[row] = v;
-    if (p.lse_out) p.lse_out[row] = v;
+    for (int i = 0; i < n; ++i)
+      a += s.wgt[i] * p.part_o[((size_t)((c0 + i) * 2 + (i == 0)) * p.G + r) * D + tid];
+    const float sum = s.sum;
+    *out = __float2bfloat16_rn(sum == 0.f ? 0.f : a / sum);
+    if (tid == 0) {
+      const float v = (s.top + log2f(sum)) * kPaLn2;
+      p.lse[row] = v;
+      if (p.lse_out) p.lse_out[row] = v;
+    }
   }
+  pa_join_sync<D>();   // `s` is free
+}
+
+// One CTA of D threads per (sequence, head).
+template <int D>
+__global__ void __launch_bounds__(D) paged_attn_combine_kernel(const PagedAttnParams p) {
+  __shared__ PaJoin s;
+  pdl_launch_dependents();
+  pa_join_row<D>(p, blockIdx.x, threadIdx.x, s, true);
 }
 
 // ----------------------------------------------------------------- weights --

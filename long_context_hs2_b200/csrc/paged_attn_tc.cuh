@@ -6,11 +6,14 @@
 //   S^T[128 positions][rows]  = K_tile . Q^T      (M = 128 positions)
 //   O^T[128 d][rows]         += V_tile^T . P^T    (M = 128 d, V read MN-major)
 // with NR = 16 or 32 rows (the G heads of one K/V head) as the MMAs' N.  TMEM
-// lane = position in S^T, so a softmax thread owns one position and 8 rows: the
-// mask is a predicate of the thread, E4M3 scales are two scalars of the thread,
-// and the exponentials need no exchange.  Row references are registers, the same
-// in all threads of a group of 8 rows; they are raised (O and the sums rescaled)
+// lane = position in S^T, so a softmax thread owns one position and half of the
+// rows: the mask is a predicate of the thread, E4M3 scales are two scalars of the
+// thread, and the exponentials need no exchange.  Row references are registers,
+// the same in all threads of a row half; they are raised (O and the sums rescaled)
 // only when a logit passes one by 2^8, agreed on by a barrier with an OR.
+// A tile's chain (S^T, softmax, P, O^T) is latency, about 2,500 cycles, so two run
+// at once: even and odd tiles of a share belong to two sets of softmax warps with
+// references, sums and an O^T of their own, joined when an item ends.
 //
 // E4M3.  K's codes go to the tensor cores as they are (kind::f8f6f4); the queries
 // are split into two E4M3 terms instead, extra rows of the MMA's N: scaled by a
@@ -20,9 +23,9 @@
 // exponent: P = 2^(x + log2 v_scale - ref), and the row sum takes P / v_scale; so
 // P stays in f16's range whatever the scales are.
 //
-// Warp roles: 0 TMA producer, 1 MMA issuer, 2-3 queries, then the softmax warps
-// (warp w: TMEM lanes 32 (w % 4) .., rows of group (w - 4) / 4), then E4M3's
-// converters.
+// Warp roles: 0 TMA producer, 1 S^T and 3 O^T issuer, 2 queries, 4-11 and 12-19 the two
+// softmax sets (warp w: TMEM lanes 32 (w % 4) .., row half (w - 4) / 4 % 2), 20-23
+// E4M3's converters.
 #pragma once
 
 #include "fp8_gemm.cuh"
@@ -31,35 +34,49 @@
 namespace hs2 {
 
 constexpr float kPtMinScale = 1e-30f;   // least |v_scale| in the exponent
-constexpr int kPtRows = 8;              // rows of a softmax thread
+constexpr int kPtSet = 8;               // softmax warps of a set
 
 template <int NR, bool FP8>
 struct PtSmem {
-  static constexpr int kGroups = NR / kPtRows;                   // row groups of 4 softmax warps
-  static constexpr int kSoftmax = 4 * kGroups;                   // softmax warps
-  static constexpr int kThreads = 32 * (4 + kSoftmax + (FP8 ? 4 : 0));
+  static constexpr int kThreads = 32 * (4 + 2 * kPtSet + (FP8 ? 4 : 0));
+  // rings: K tiles (with the tile's scales and mask), V tiles, E4M3's f16 V tiles
   static constexpr int kTile = 128 * 128 * (FP8 ? 1 : 2);
-  static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = FP8 ? 4 : 3;
+  static constexpr int kK = FP8 ? 4 : 3, kV = FP8 ? 2 : 3, kH = FP8 ? 3 : 0;
   static constexpr int kQTerms = FP8 ? 2 : 1;
-  static constexpr int kV16Off = kStages * kStage;               // E4M3: two f16 V tiles
-  static constexpr int kQOff = kV16Off + (FP8 ? 2 * 32768 : 0);
+  static constexpr int kVOff = kK * kTile;
+  static constexpr int kHOff = kVOff + kV * kTile;
+  static constexpr int kQOff = kHOff + kH * 32768;
   static constexpr int kQBytes = NR * 256;                       // bf16, or two terms of codes
   static constexpr int kPOff = kQOff + kQBytes;
-  static constexpr int kPBytes = NR * 256;
-  static constexpr int kMetaOff = kPOff + 2 * kPBytes;           // per stage: scales, mask
+  static constexpr int kPBytes = NR * 256;                       // P^T of a set
+  static constexpr int kMetaOff = kPOff + 2 * kPBytes;
   static constexpr int kMetaBytes = (FP8 ? 1024 : 0) + 64;
-  static constexpr int kRsOff = kMetaOff + kStages * kMetaBytes; // float [4][NR]: queries' scales
-  static constexpr int kRedOff = kRsOff + 4 * NR * 4;            // float [4][NR]
-  static constexpr int kBarOff = kRedOff + 4 * NR * 4;
-  static constexpr int kBars = 3 * kStages + 18;
+  static constexpr int kRsOff = kMetaOff + kK * kMetaBytes;      // float [2][NR]: queries' scales
+  static constexpr int kRedOff = kRsOff + 2 * NR * 4;            // float [2 sets][4][NR]
+  static constexpr int kRefOff = kRedOff + 8 * NR * 4;           // float [2 sets][NR]
+  static constexpr int kBarOff = kRefOff + 2 * NR * 4;
+  static constexpr int kBars = 2 * kK + 2 * kV + 2 * kH + 18;
   static constexpr int kSlotOff = kBarOff + kBars * 8;
   static constexpr int kWorkOff = (kSlotOff + 16 + 15) / 16 * 16;   // int4
   static constexpr int kBytes = kWorkOff + 64 + 1024;
-  // TMEM columns
-  static constexpr int kSCols = kQTerms * NR, kOCol = 2 * kSCols;
-  static constexpr int kTmem = kOCol + NR <= 64 ? 64 : kOCol + NR <= 128 ? 128 : 256;
+  // TMEM columns: S^T of four tiles, O^T of the two sets
+  static constexpr int kSCols = kQTerms * NR, kOCol = 4 * kSCols;
+  static constexpr int kNeed = kOCol + 2 * NR;
+  static constexpr int kTmem = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+  // registers: of the launch's kRegs a thread, warps 0-3 and the converters give
+  // some to the softmax warps
+  static constexpr int kRegs = FP8 ? 80 : 96, kFew = FP8 ? 56 : 64, kConv = 40,
+                       kMany = FP8 ? 96 : 104;
+  static_assert(128 * kFew + 512 * kMany + (FP8 ? 128 * kConv : 0) <= kThreads * kRegs,
+                "shares of the registers");
+  static_assert(2 * kPBytes >= NR * 128 * 4, "a set's O^T fits the two P^T buffers");
 };
+
+// NC (8 or 16) consecutive columns.
+template <int NC>
+__device__ __forceinline__ void tmem_ldc(uint32_t taddr, float* v);
+template <int NC>
+__device__ __forceinline__ void tmem_stc(uint32_t taddr, const float* v);
 
 // 8 consecutive fp32 columns of this warp's 32 TMEM lanes.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
@@ -78,19 +95,32 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
                "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
                : "memory");
 }
-// Barrier, and barrier with OR, of a row group (128 threads, named 1 + group).
-__device__ __forceinline__ void pt_group_sync(int group) {
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+template <>
+__device__ __forceinline__ void tmem_ldc<8>(uint32_t taddr, float* v) { tmem_ld8(taddr, v); }
+template <>
+__device__ __forceinline__ void tmem_ldc<16>(uint32_t taddr, float* v) { tmem_ld16(taddr, v); }
+template <>
+__device__ __forceinline__ void tmem_stc<8>(uint32_t taddr, const float* v) { tmem_st8(taddr, v); }
+template <>
+__device__ __forceinline__ void tmem_stc<16>(uint32_t taddr, const float* v) { tmem_st16(taddr, v); }
+
+// Barrier, and barrier with OR, of a row half of a set (128 threads, named 1-4),
+// and a barrier of both sets.
+__device__ __forceinline__ void pt_half_sync(int id) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + id) : "memory");
 }
-__device__ __forceinline__ bool pt_group_any(int group, bool v) {
+__device__ __forceinline__ bool pt_half_any(int id, bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(1 + group), "r"((uint32_t)v)
+      : "r"(1 + id), "r"((uint32_t)v)
       : "memory");
   return r != 0;
+}
+__device__ __forceinline__ void pt_sets_sync() {
+  asm volatile("bar.sync 5, %0;" ::"n"(64 * kPtSet) : "memory");
 }
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
   const uint32_t h = e4m3x2_to_f16x2(two);
@@ -99,22 +129,32 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
 __device__ __forceinline__ uint32_t float2_to_e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
+// Maximum over the warp (NaN is left out).
+__device__ __forceinline__ float warp_max_f32(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// The producer warp: tile t of an item into stage st (K, scales and mask on
-// kfull, V on vfull).  ids[0]: the page of the lane's run, as in pa_fetch.
-template <int NR, bool FP8, bool KONLY>
-__device__ __forceinline__ void pt_fetch(const PagedCache& c, const CUtensorMap* km,
-                                         const CUtensorMap* vm, uint8_t* kt, uint8_t* meta,
-                                         uint64_t* kfull, uint64_t* vfull, int id, int t, int len,
-                                         int head, int* slots, uint64_t kpol, uint64_t vpol) {
-  using SM = PtSmem<NR, FP8>;
+// One lane's run of a tile: its page's rows [j0 + lane * rows, + rows), if any.
+struct PtRun {
+  int slot;        // of its first row
+  bool ok;
+};
+// The producer warp: tile t's K rows, scales and mask into a K slot.  id: the page
+// of the lane's run.  KONLY: the weights' pass, which wants every position's slot
+// and no v_scale.
+template <bool FP8, bool KONLY>
+__device__ __forceinline__ PtRun pt_fetch_k(const PagedCache& c, const CUtensorMap* km,
+                                            uint8_t* kt, uint8_t* meta, uint64_t* full, int id,
+                                            int t, int len, int head, int* slots, uint64_t pol) {
   const int lane = threadIdx.x & 31;
-  const int shift = min(c.page_shift, 7), runs = kPaTile >> shift, rows = 1 << shift;
+  const int shift = min(c.page_shift, 7), rows = 1 << shift;
   const int page_mask = (1 << c.page_shift) - 1, j0 = t * kPaTile;
   unsigned live[4];
 #pragma unroll
@@ -135,24 +175,33 @@ __device__ __forceinline__ void pt_fetch(const PagedCache& c, const CUtensorMap*
   if (lane < 4)
     mask[lane] = lane == 0 ? live[0] : lane == 1 ? live[1] : lane == 2 ? live[2] : live[3];
   __syncwarp();
-  const bool ok = lane < runs && j0 + lane * rows < len && id >= 0;
-  const unsigned bytes = __popc(__ballot_sync(0xffffffffu, ok)) * rows * (SM::kTile / 128);
-  if (lane == 0) {
-    mbar_arrive_expect_tx(kfull, bytes);
-    if (!KONLY) mbar_arrive_expect_tx(vfull, bytes);
-  }
+  PtRun r;
+  r.ok = lane < (kPaTile >> shift) && j0 + lane * rows < len && id >= 0;
+  r.slot = (int)(((long long)id << c.page_shift) + ((j0 + lane * rows) & page_mask));
+  const unsigned n = __popc(__ballot_sync(0xffffffffu, r.ok));
+  if (lane == 0) mbar_arrive_expect_tx(full, n * rows * (FP8 ? 128 : 256));
   __syncwarp();
-  if (ok) {
-    const int z = (int)(((long long)id << c.page_shift) + ((j0 + lane * rows) & page_mask));
+  if (r.ok) {
     const uint32_t dst = smem_u32(kt) + lane * rows * 128;
-    tma_load_3d(dst, km, kfull, 0, head, z, kpol);
-    if (!FP8) tma_load_3d(dst + 16384, km, kfull, 64, head, z, kpol);
-    if (!KONLY) {
-      tma_load_3d(dst + SM::kTile, vm, vfull, 0, head, z, vpol);
-      if (!FP8) tma_load_3d(dst + SM::kTile + 16384, vm, vfull, 64, head, z, vpol);
-    }
+    tma_load_3d(dst, km, full, 0, head, r.slot, pol);
+    if (!FP8) tma_load_3d(dst + 16384, km, full, 64, head, r.slot, pol);
   }
-  if (FP8) cp_async_arrive(kfull);
+  if (FP8) cp_async_arrive(full);
+  return r;
+}
+// The same tile's V rows into a V slot.
+template <bool FP8>
+__device__ __forceinline__ void pt_fetch_v(const PagedCache& c, const CUtensorMap* vm, uint8_t* vt,
+                                           uint64_t* full, const PtRun& r, int head, uint64_t pol) {
+  const int lane = threadIdx.x & 31, rows = 1 << min(c.page_shift, 7);
+  const unsigned n = __popc(__ballot_sync(0xffffffffu, r.ok));
+  if (lane == 0) mbar_arrive_expect_tx(full, n * rows * (FP8 ? 128 : 256));
+  __syncwarp();
+  if (r.ok) {
+    const uint32_t dst = smem_u32(vt) + lane * rows * 128;
+    tma_load_3d(dst, vm, full, 0, head, r.slot, pol);
+    if (!FP8) tma_load_3d(dst + 16384, vm, full, 64, head, r.slot, pol);
+  }
 }
 
 // The producer's view of a sequence's page list: 32 entries a load, the next 32
@@ -188,53 +237,57 @@ struct PtPages {
   }
 };
 
-// The query warps (64 threads): an item's rows from global memory ...
-template <int NR>
-__device__ __forceinline__ void pt_read_q(const __nv_bfloat16* q, int G, int tid, uint4* w) {
-#pragma unroll
-  for (int i = 0; i < NR / 4; ++i) {
-    const int r = i * 4 + (tid >> 4), ch = tid & 15;
-    w[i] = r < G ? *reinterpret_cast<const uint4*>(q + (size_t)r * 128 + ch * 8)
-                 : make_uint4(0, 0, 0, 0);
-  }
-}
-// ... and into shared memory as the MMA's B operand.
+// The query warp: an item's rows from global memory into shared memory as the
+// MMA's B operand; E4M3: as two terms, the rows' scales beside them.  (Rolled: it
+// runs once an item, and long code that runs once is paid for in instruction
+// fetches.)
 template <int NR, bool FP8>
-__device__ __forceinline__ void pt_write_q(uint8_t* qs, float* row_scale, int tid, const uint4* w) {
-  const int ch = tid & 15;
+__device__ __forceinline__ void pt_stage_q(const __nv_bfloat16* q, int G, uint8_t* qs,
+                                           float* row_scale) {
+  const int lane = threadIdx.x & 31, ch = lane & 15;
+#pragma unroll 1
+  for (int i0 = 0; i0 < NR / 2; i0 += 4) {
+    uint4 w[4];
 #pragma unroll
-  for (int i = 0; i < NR / 4; ++i) {
-    const int r = i * 4 + (tid >> 4);
-    if (!FP8) {
-      *reinterpret_cast<uint4*>(qs + sw128_offset(r, ch * 16, NR)) = w[i];
-    } else {
-      const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      float f[8], amax = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const int r = (i0 + i) * 2 + (lane >> 4);
+      w[i] = r < G ? *reinterpret_cast<const uint4*>(q + (size_t)r * 128 + ch * 8)
+                   : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 v = bf16x2_to_float2(ww[k]);
-        f[2 * k] = v.x;
-        f[2 * k + 1] = v.y;
-        amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+    for (int i = 0; i < 4; ++i) {
+      const int r = (i0 + i) * 2 + (lane >> 4);
+      if (!FP8) {
+        *reinterpret_cast<uint4*>(qs + sw128_offset(r, ch * 16, NR)) = w[i];
+      } else {
+        const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        float f[8], amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = bf16x2_to_float2(ww[k]);
+          f[2 * k] = v.x;
+          f[2 * k + 1] = v.y;
+          amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e = amax > 0.f ? max(-110, (int)(__float_as_uint(amax) >> 23) - 127) : 0;
+        const float down = __uint_as_float((uint32_t)(134 - e) << 23);   // 2^(7 - e)
+        if (ch == 0) row_scale[r] = __uint_as_float((uint32_t)(120 + e) << 23);
+        uint32_t t1[2] = {0, 0}, t2[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = f[2 * k] * down, b = f[2 * k + 1] * down;
+          const uint32_t c1 = float2_to_e4m3x2(a, b);
+          const float2 back = e4m3x2_to_float2(c1);
+          const uint32_t c2 = float2_to_e4m3x2((a - back.x) * 16.f, (b - back.y) * 16.f);
+          t1[k >> 1] |= c1 << ((k & 1) * 16);
+          t2[k >> 1] |= c2 << ((k & 1) * 16);
+        }
+        const uint32_t at = r * 128 + (((ch >> 1) ^ (r & 7)) << 4) + (ch & 1) * 8;
+        *reinterpret_cast<uint2*>(qs + at) = make_uint2(t1[0], t1[1]);
+        *reinterpret_cast<uint2*>(qs + NR * 128 + at) = make_uint2(t2[0], t2[1]);
       }
-#pragma unroll
-      for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const int e = amax > 0.f ? max(-110, (int)(__float_as_uint(amax) >> 23) - 127) : 0;
-      const float down = __uint_as_float((uint32_t)(134 - e) << 23);   // 2^(7 - e)
-      if (ch == 0) row_scale[r] = __uint_as_float((uint32_t)(120 + e) << 23);
-      uint32_t t1[2] = {0, 0}, t2[2] = {0, 0};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float a = f[2 * k] * down, b = f[2 * k + 1] * down;
-        const uint32_t c1 = float2_to_e4m3x2(a, b);
-        const float2 back = e4m3x2_to_float2(c1);
-        const uint32_t c2 = float2_to_e4m3x2((a - back.x) * 16.f, (b - back.y) * 16.f);
-        t1[k >> 1] |= c1 << ((k & 1) * 16);
-        t2[k >> 1] |= c2 << ((k & 1) * 16);
-      }
-      const uint32_t at = r * 128 + (((ch >> 1) ^ (r & 7)) << 4) + (ch & 1) * 8;
-      *reinterpret_cast<uint2*>(qs + at) = make_uint2(t1[0], t1[1]);
-      *reinterpret_cast<uint2*>(qs + NR * 128 + at) = make_uint2(t2[0], t2[1]);
     }
   }
 }
@@ -274,51 +327,63 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap km,
                          const __grid_constant__ CUtensorMap vm, const PagedAttnParams p) {
   using SM = PtSmem<NR, FP8>;
-  constexpr int NC = kPtRows, S = SM::kStages, NW = SM::kSoftmax;
+  constexpr int NC = NR / 2, KN = SM::kK, VN = SM::kV, HN = FP8 ? SM::kH : 1;
   static_assert(SM::kBytes <= 232448, "shared memory per CTA");
   static_assert(SM::kWorkOff % 16 == 0 && SM::kBarOff % 8 == 0 && SM::kMetaOff % 16 == 0 &&
                     SM::kMetaBytes % 16 == 0, "alignment of shared words");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
-  uint64_t* vfull = kfull + S;
-  uint64_t* empty = vfull + S;
-  uint64_t* s_full = empty + S;      // [2]
-  uint64_t* s_empty = s_full + 2;    // [2]
-  uint64_t* p_full = s_empty + 2;    // [2]
-  uint64_t* pv_done = p_full + 2;    // [2]
-  uint64_t* v16_full = pv_done + 2;  // [2] E4M3: a V tile is f16
-  uint64_t* q_full = v16_full + 2;
+  uint64_t* kempty = kfull + KN;
+  uint64_t* vfull = kempty + KN;
+  uint64_t* vempty = vfull + VN;
+  uint64_t* h_full = vempty + VN;    // E4M3: a V tile is f16
+  uint64_t* h_empty = h_full + SM::kH;
+  uint64_t* s_full = h_empty + SM::kH;   // [4]
+  uint64_t* s_empty = s_full + 4;    // [4]
+  uint64_t* p_full = s_empty + 4;    // [2 sets]
+  uint64_t* pv_done = p_full + 2;    // [2 sets]
+  uint64_t* q_full = pv_done + 2;
   uint64_t* q_free = q_full + 1;
-  // Row scales of item i of the share are in buffer i % 4: the queries of item i
-  // are written after the last S^T of item i - 1, so after the softmax warps read
-  // the S^T two tiles before that one: they are at most three items behind, which
-  // neither a buffer's reuse nor a barrier's phase can outrun.
-  uint64_t* rs_full = q_free + 1;    // [4]
+  // E4M3: the queries' row scales of item i of the share, in buffer i % 2
+  uint64_t* rs_full = q_free + 1;    // [2]
+  uint64_t* rs_free = rs_full + 2;   // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kSlotOff);
   int4* work = reinterpret_cast<int4*>(smem + SM::kWorkOff);
   float* row_scale = reinterpret_cast<float*>(smem + SM::kRsOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   pdl_launch_dependents();
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&km);
+    tma_prefetch_desc(&vm);
+  }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < KN; ++i) {
       mbar_init(&kfull[i], pa_full_count(FP8, false));
+      // S^T is done with K, a softmax set (and the converters) with scales and mask
+      mbar_init(&kempty[i], 1 + kPtSet + (FP8 ? 4 : 0));
+    }
+    for (int i = 0; i < VN; ++i) {
       mbar_init(&vfull[i], 1);
-      // bf16: O^T is done with the stage; E4M3: S^T is done with K, V is
-      // converted, the softmax warps have read the scales
-      mbar_init(&empty[i], FP8 ? 1 + 4 + NW : 1);
+      mbar_init(&vempty[i], FP8 ? 4 : 1);   // converted, or O^T is done with V
+    }
+    for (int i = 0; i < SM::kH; ++i) {
+      mbar_init(&h_full[i], 4);
+      mbar_init(&h_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], kPtSet);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], NW);
-      mbar_init(&p_full[i], NW);
+      mbar_init(&p_full[i], kPtSet);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&v16_full[i], 4);
+      mbar_init(&rs_full[i], 1);
+      mbar_init(&rs_free[i], 2 * kPtSet);
     }
-    mbar_init(q_full, 2);
+    mbar_init(q_full, 1);
     mbar_init(q_free, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&rs_full[i], 2);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -336,191 +401,198 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
   PaWalk w;
   if (any) w.start(p.c, *work);
 
-  if (any && warp == 0) {
-    // ----------------------------------------------------------- producer
-    const uint64_t kpol = policy_evict_normal(), vpol = policy_evict_first();
-    uint32_t it = 0;
-    bool ok = true;
-    do {
-      PtPages pages;
-      pages.start(p.c, w.b, w.t0, w.len);
-      for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const int st = it % S;
-        if (it >= (uint32_t)S) ok = mbar_wait(&empty[st], ((it / S) - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        pt_fetch<NR, FP8, false>(p.c, &km, &vm, smem + st * SM::kStage,
-                                 smem + SM::kMetaOff + st * SM::kMetaBytes, &kfull[st], &vfull[st],
-                                 pages.at(p.c, t), t, w.len, w.head, nullptr, kpol, vpol);
-      }
-    } while (ok && w.next(p.c, p.c.heads));
-  } else if (any && warp == 1) {
-    // --------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t q_addr = smem_u32(smem + SM::kQOff), p_addr = smem_u32(smem + SM::kPOff);
-      uint32_t it = 0, seg = 0;
-      bool ok = true, pending = false, pending_first = false;
-      auto pv = [&](uint32_t i, bool first) {
-        const int st = i % S, bb = i & 1;
-        if (!mbar_wait(&p_full[bb], (i >> 1) & 1) ||
-            !(FP8 ? mbar_wait(&v16_full[bb], (i >> 1) & 1) : mbar_wait(&vfull[st], (i / S) & 1)))
-          return false;
-        tc_fence_after();
-        pt_issue_pv<NR, FP8>(tmem + SM::kOCol,
-                             smem_u32(FP8 ? smem + SM::kV16Off + bb * 32768
-                                          : smem + st * SM::kStage + SM::kTile),
-                             p_addr + bb * SM::kPBytes, !first);
-        tc_commit(&pv_done[bb]);
-        if (!FP8) tc_commit(&empty[st]);
-        return true;
-      };
+  if (warp < 4) {
+    regs_give_up<SM::kFew>();
+    if (any && warp == 0) {
+      // --------------------------------------------------------- producer
+      const uint64_t kpol = policy_evict_normal(), vpol = policy_evict_first();
+      uint32_t it = 0;
+      bool ok = true;
       do {
-        ok = mbar_wait(q_full, seg & 1);
-        for (int t = w.t0; t < w.t1 && ok; ++t, ++it) {
-          const int st = it % S, bb = it & 1;
-          if (!mbar_wait(&kfull[st], (it / S) & 1) ||
-              (it >= 2 && !mbar_wait(&s_empty[bb], ((it - 2) >> 1) & 1))) {
-            ok = false;
-            break;
+        PtPages pages;
+        pages.start(p.c, w.b, w.t0, w.len);
+        for (int t = w.t0; t < w.t1; ++t, ++it) {
+          const int ks = it % KN, vs = it % VN;
+          if (it >= (uint32_t)KN) ok = mbar_wait(&kempty[ks], ((it / KN) - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const PtRun r = pt_fetch_k<FP8, false>(
+              p.c, &km, smem + ks * SM::kTile, smem + SM::kMetaOff + ks * SM::kMetaBytes,
+              &kfull[ks], pages.at(p.c, t), t, w.len, w.head, nullptr, kpol);
+          if (it >= (uint32_t)VN) ok = mbar_wait(&vempty[vs], ((it / VN) - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          pt_fetch_v<FP8>(p.c, &vm, smem + SM::kVOff + vs * SM::kTile, &vfull[vs], r, w.head, vpol);
+        }
+      } while (ok && w.next(p.c, p.c.heads));
+    } else if (any && warp == 1) {
+      // ------------------------------------------- S^T: up to four tiles ahead
+      if (lane == 0) {
+        const uint32_t q_addr = smem_u32(smem + SM::kQOff);
+        uint32_t it = 0, seg = 0;
+        bool ok = true;
+        do {
+          ok = mbar_wait(q_full, seg & 1);
+          for (int t = w.t0; t < w.t1 && ok; ++t, ++it) {
+            const uint32_t ks = it % KN, sb = it & 3;
+            ok = mbar_wait(&kfull[ks], (it / KN) & 1) &&
+                 (it < 4 || mbar_wait(&s_empty[sb], ((it >> 2) & 1) ^ 1));
+            if (!ok) break;
+            tc_fence_after();
+            pt_issue_qk<NR, FP8>(tmem + sb * SM::kSCols, smem_u32(smem + ks * SM::kTile), q_addr);
+            tc_commit(&s_full[sb]);
+            tc_commit(&kempty[ks]);
           }
-          tc_fence_after();
-          pt_issue_qk<NR, FP8>(tmem + bb * SM::kSCols, smem_u32(smem + st * SM::kStage), q_addr);
-          tc_commit(&s_full[bb]);
-          if (FP8) tc_commit(&empty[st]);
-          if (t + 1 == w.t1) tc_commit(q_free);
-          if (pending) ok = pv(it - 1, pending_first);
-          pending = true;
-          pending_first = t == w.t0;
+          tc_commit(q_free);
+          ++seg;
+        } while (ok && w.next(p.c, p.c.heads));
+      }
+    } else if (any && warp == 3) {
+      // ------------------------------------------------------------- O^T
+      if (lane == 0) {
+        const uint32_t p_addr = smem_u32(smem + SM::kPOff);
+        uint32_t it = 0;
+        bool ok = true;
+        do {
+          for (int t = w.t0; t < w.t1 && ok; ++t, ++it) {
+            const uint32_t vs = it % VN, hs = it % HN, set = it & 1;
+            ok = (FP8 ? mbar_wait(&h_full[hs], (it / HN) & 1)
+                      : mbar_wait(&vfull[vs], (it / VN) & 1)) &&
+                 mbar_wait(&p_full[set], (it >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            pt_issue_pv<NR, FP8>(tmem + SM::kOCol + set * NR,
+                                 smem_u32(FP8 ? smem + SM::kHOff + hs * 32768
+                                              : smem + SM::kVOff + vs * SM::kTile),
+                                 p_addr + set * SM::kPBytes, t - w.t0 >= 2);
+            tc_commit(&pv_done[set]);
+            tc_commit(FP8 ? &h_empty[hs] : &vempty[vs]);
+          }
+        } while (ok && w.next(p.c, p.c.heads));
+      }
+    } else if (any) {
+      // ------------------------------------------------------------ queries
+      uint32_t seg = 0;
+      bool dead = false;
+      do {
+        if (seg > 0 && !dead) dead = !mbar_wait(q_free, (seg - 1) & 1);
+        if (FP8 && seg > 1 && !dead) dead = !mbar_wait(&rs_free[seg & 1], ((seg >> 1) - 1) & 1);
+        pt_stage_q<NR, FP8>(p.q + ((size_t)w.b * p.H + (size_t)w.head * p.G) * 128, p.G,
+                            smem + SM::kQOff, row_scale + (seg & 1) * NR);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(q_full);
+          if (FP8) mbar_arrive(&rs_full[seg & 1]);
         }
         ++seg;
-      } while (ok && w.next(p.c, p.c.heads));
-      if (ok && pending) pv(it - 1, pending_first);
+      } while (w.next(p.c, p.c.heads));
     }
-  } else if (any && warp < 4) {
-    // -------------------------------------------------------------- queries
-    const int tid = threadIdx.x - 64;
-    uint32_t seg = 0;
+  } else if (FP8 && warp >= 4 + 2 * kPtSet) {
+    // ------------------------------------------------------- V to f16 tiles
+    regs_give_up<SM::kConv>();
+    const int row = threadIdx.x - 32 * (4 + 2 * kPtSet);
+    const uint32_t total = (uint32_t)(work->y - work->x);
     bool dead = false;
-    do {
-      uint4 qw[NR / 4];
-      pt_read_q<NR>(p.q + ((size_t)w.b * p.H + (size_t)w.head * p.G) * 128, p.G, tid, qw);
-      if (seg > 0 && !dead) dead = !mbar_wait(q_free, (seg - 1) & 1);
-      pt_write_q<NR, FP8>(smem + SM::kQOff, row_scale + (seg & 3) * NR, tid, qw);
+    for (uint32_t it = 0; any && it < total; ++it) {
+      const int ks = it % KN, vs = it % VN, hs = it % HN;
+      if (it >= (uint32_t)HN && !dead) dead = !mbar_wait(&h_empty[hs], ((it / HN) - 1) & 1);
+      if (!dead) dead = !mbar_wait(&vfull[vs], (it / VN) & 1);   // after the mask was written
+      const unsigned word = reinterpret_cast<const unsigned*>(
+          smem + SM::kMetaOff + ks * SM::kMetaBytes + 1024)[row >> 5];
+      const uint8_t* src = smem + SM::kVOff + vs * SM::kTile + row * 128;
+      uint8_t* dst = smem + SM::kHOff + hs * 32768;
+      // rows that are not positions become zeros, whatever they hold
+      const uint32_t keep = word >> lane & 1u ? 0xffffffffu : 0u;
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) {
+        const uint4 c = *reinterpret_cast<const uint4*>(src + ((ch ^ (row & 7)) << 4));
+        const uint32_t cw[4] = {c.x & keep, c.y & keep, c.z & keep, c.w & keep};
+        uint32_t h[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          h[2 * q] = e4m3x2_to_f16x2(cw[q] & 0xffffu);
+          h[2 * q + 1] = e4m3x2_to_f16x2(cw[q] >> 16);
+        }
+        *reinterpret_cast<uint4*>(dst + sw128_offset(row, ch * 32, 128)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(dst + sw128_offset(row, ch * 32 + 16, 128)) =
+            make_uint4(h[4], h[5], h[6], h[7]);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(q_full);
-        mbar_arrive(&rs_full[seg & 3]);
+        mbar_arrive(&kempty[ks]);
+        mbar_arrive(&vempty[vs]);
+        mbar_arrive(&h_full[hs]);
       }
-      ++seg;
-    } while (w.next(p.c, p.c.heads));
-  } else if (FP8 && any && warp >= 4 + NW) {
-    // ------------------------------------------------------- V to f16 tiles
-    const int row = threadIdx.x - 32 * (4 + NW);
-    uint32_t it = 0;
-    bool dead = false;
-    do {
-      for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const int st = it % S, bb = it & 1;
-        if (!dead) dead = !mbar_wait(&kfull[st], (it / S) & 1);    // the mask
-        if (!dead) dead = !mbar_wait(&vfull[st], (it / S) & 1);
-        const unsigned word = reinterpret_cast<const unsigned*>(
-            smem + SM::kMetaOff + st * SM::kMetaBytes + 1024)[row >> 5];
-        const bool live = word >> lane & 1u;
-        const uint8_t* src = smem + st * SM::kStage + SM::kTile + row * 128;
-        uint4 c[8];
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch)
-          c[ch] = *reinterpret_cast<const uint4*>(src + ((ch ^ (row & 7)) << 4));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
-        if (it >= 2 && !dead) dead = !mbar_wait(&pv_done[bb], ((it - 2) >> 1) & 1);
-        uint8_t* dst = smem + SM::kV16Off + bb * 32768;
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          // rows that are not positions become zeros, whatever they hold
-          const uint32_t cw[4] = {c[ch].x, c[ch].y, c[ch].z, c[ch].w};
-          uint32_t h[8];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            h[2 * q] = live ? e4m3x2_to_f16x2(cw[q] & 0xffffu) : 0u;
-            h[2 * q + 1] = live ? e4m3x2_to_f16x2(cw[q] >> 16) : 0u;
-          }
-          *reinterpret_cast<uint4*>(dst + sw128_offset(row, ch * 32, 128)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + sw128_offset(row, ch * 32 + 16, 128)) =
-              make_uint4(h[4], h[5], h[6], h[7]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v16_full[bb]);
-      }
-    } while (w.next(p.c, p.c.heads));
-  } else if (any) {
+    }
+  } else {
     // -------------------------------------------------------------- softmax
-    const int wq = warp & 3, group = (warp - 4) >> 2, c0 = group * NC;
+    regs_take<SM::kMany>();
+    const int wq = warp & 3, set = (warp - 4) >> 3, half = (warp - 4) >> 2 & 1, c0 = half * NC;
+    const int id = set * 2 + half;                  // named barrier
     const int key = wq * 32 + lane;                 // position in the tile; d of O^T
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-    float* red = reinterpret_cast<float*>(smem + SM::kRedOff);
+    float* red = reinterpret_cast<float*>(smem + SM::kRedOff) + set * 4 * NR;
+    float* ref = reinterpret_cast<float*>(smem + SM::kRefOff);        // [set][row]
     // where this lane's two positions of rows c0 + (lane & 1), + 2, .. go in P^T
-    uint8_t* const p_row = smem + SM::kPOff + (key >> 6) * (NR * 128) + (c0 + (lane & 1)) * 128 +
-                           (key & 6) * 2;
+    uint8_t* const p_row = smem + SM::kPOff + set * SM::kPBytes + (key >> 6) * (NR * 128) +
+                           (c0 + (lane & 1)) * 128 + (key & 6) * 2;
     const int p_chunk = (key & 63) >> 3;
-    uint32_t it = 0, seg = 0;
+    uint32_t it0 = 0, seg = 0;                      // the item's first tile, counted over the share
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       // after a wait that gave up (reported), no more waits: every barrier is still met
       if (!dead) dead = !mbar_wait(bar, parity);
     };
-    do {
-      float mref[NC], l[NC], f[NC];
-      if (FP8) wait(&rs_full[seg & 3], (seg >> 2) & 1);
+    if (any) do {
+      float mref[NC], l[NC];
+      if (FP8) wait(&rs_full[seg & 1], (seg >> 1) & 1);
+      const float* f = row_scale + (seg & 1) * NR + c0;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        mref[i] = 0.f;
-        l[i] = 0.f;
-        f[i] = FP8 ? row_scale[(seg & 3) * NR + c0 + i] * p.scale_log2 : p.scale_log2;
-      }
+      for (int i = 0; i < NC; ++i) mref[i] = l[i] = 0.f;
       bool fresh = true;                            // no position met yet: no references
-      for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const int st = it % S, bb = it & 1;
+      const int n = w.t1 - w.t0, skip = (it0 & 1) ^ set;
+      for (uint32_t it = it0 + skip; it < it0 + n; it += 2) {
+        const int st = it % KN, sb = it & 3;
+        const uint32_t ph = (it >> 1) & 1;
         const uint8_t* meta = smem + SM::kMetaOff + st * SM::kMetaBytes;
-        wait(&kfull[st], (it / S) & 1);             // scales and mask
+        wait(&s_full[sb], (it >> 2) & 1);
+        tc_fence_after();
+        float d[NC];                                // log2 of p, relative to the references
+        float d2[FP8 ? NC : 1];
+        const uint32_t s_at = lanes + sb * SM::kSCols + c0;
+        tmem_ldc<NC>(s_at, d);
+        if (FP8) tmem_ldc<NC>(s_at + NR, d2);
+        wait(&kfull[st], (it / KN) & 1);            // scales and mask
         const unsigned word =
             reinterpret_cast<const unsigned*>(meta + (FP8 ? 1024 : 0))[wq];
         const bool live = word >> lane & 1u;
         float ks = 1.f, lv = 0.f, inv = 1.f;
         uint32_t flip = 0;
         if (FP8) {
-          ks = reinterpret_cast<const float*>(meta)[key];
+          ks = reinterpret_cast<const float*>(meta)[key] * p.scale_log2;
           const float vs = reinterpret_cast<const float*>(meta + 512)[key];
           const float a = fmaxf(fabsf(vs), kPtMinScale);
           flip = vs < 0.f ? 0x80008000u : 0u;
           lv = __log2f(a);
           inv = fast_rcp(a);
         }
-        wait(&s_full[bb], (it >> 1) & 1);
-        tc_fence_after();
-        float d[NC];                                // log2 of p, relative to the references
-        tmem_ld8(lanes + bb * SM::kSCols + c0, d);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kempty[st]);
+        tmem_ld_wait();
         if (FP8) {
-          float d2[NC];
-          tmem_ld8(lanes + bb * SM::kSCols + NR + c0, d2);
-          tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < NC; ++i)
             d[i] = fmaf(fmaf(d2[i], 0.0625f, d[i]) * f[i], ks, lv - mref[i]);
         } else {
-          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < NC; ++i) d[i] = fmaf(d[i], f[i], -mref[i]);
+          for (int i = 0; i < NC; ++i) d[i] = fmaf(d[i], p.scale_log2, -mref[i]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s_empty[bb]);
-          if (FP8) mbar_arrive(&empty[st]);
-        }
+        if (lane == 0) mbar_arrive(&s_empty[sb]);
         if (word != 0xffffffffu && !live) {         // replaced, not computed with
           inv = 1.f;
 #pragma unroll
@@ -529,75 +601,76 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
         float top = d[0];
 #pragma unroll
         for (int i = 1; i < NC; ++i) top = fmaxf(top, d[i]);
-        if (pt_group_any(group, fresh ? top > -INFINITY : top > kPaSlack)) {
-          // references to the tile's maxima; O and the sums follow
+        const bool raise = pt_half_any(id, fresh ? top > -INFINITY : top > kPaSlack);
+        // the set's tile before is done with O^T and P^T
+        if (it >= 2) wait(&pv_done[set], ph ^ 1);
+        if (raise) {
+          // references to the tile's maxima; O and the sums follow.  Runs a few
+          // times an item, so it is kept short in code: lane i works out row i
+          float m = 0.f;
 #pragma unroll
           for (int i = 0; i < NC; ++i) {
-            float m = d[i];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == i) red[wq * NR + c0 + i] = m;
+            const float x = warp_max_f32(d[i]);
+            m = lane == i ? x : m;
           }
-          pt_group_sync(group);
+          float* at = red + c0 + (lane & (NC - 1));
+          if (lane < NC) at[wq * NR] = m;
+          pt_half_sync(id);
+          m = fmaxf(fmaxf(at[0], at[NR]), fmaxf(at[2 * NR], at[3 * NR]));
+          if (!fresh) m = fmaxf(m, 0.f);
+          if (m == -INFINITY) m = 0.f;
+          const float shrink = fresh ? 0.f : fast_exp2(-m);
           float a[NC];
 #pragma unroll
           for (int i = 0; i < NC; ++i) {
-            float m = fmaxf(fmaxf(red[c0 + i], red[NR + c0 + i]),
-                            fmaxf(red[2 * NR + c0 + i], red[3 * NR + c0 + i]));
-            if (!fresh) m = fmaxf(m, 0.f);
-            if (m == -INFINITY) m = 0.f;
-            a[i] = fast_exp2(-m);
-            mref[i] += m;
-            d[i] -= m;
-            l[i] *= fresh ? 0.f : a[i];
+            const float mi = __shfl_sync(0xffffffffu, m, i);
+            a[i] = __shfl_sync(0xffffffffu, shrink, i);
+            mref[i] += mi;
+            d[i] -= mi;
+            l[i] *= a[i];
           }
           if (!fresh) {
-            wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
             tc_fence_after();
             float o[NC];
-            tmem_ld8(lanes + SM::kOCol + c0, o);
+            tmem_ldc<NC>(lanes + SM::kOCol + set * NR + c0, o);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < NC; ++i) o[i] *= a[i];
-            tmem_st8(lanes + SM::kOCol + c0, o);
+            tmem_stc<NC>(lanes + SM::kOCol + set * NR + c0, o);
             tmem_st_wait();
             tc_fence_before();
           }
           fresh = false;
         }
         // P
-        float e[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-          e[i] = fast_exp2(d[i]);
-          l[i] = fmaf(e[i], inv, l[i]);
+          d[i] = fast_exp2(d[i]);
+          l[i] = fmaf(d[i], inv, l[i]);
         }
-        if (it >= 2) wait(&pv_done[bb], ((it - 2) >> 1) & 1);   // P's buffer is free
 #pragma unroll
         for (int i = 0; i < NC; i += 2) {
           // two rows of one position -> two positions of one row, over 2 lanes
-          const uint32_t v = FP8 ? pack_f16(e[i], e[i + 1]) ^ flip : pack_bf16(e[i], e[i + 1]);
+          const uint32_t v = FP8 ? pack_f16(d[i], d[i + 1]) ^ flip : pack_bf16(d[i], d[i + 1]);
           const uint32_t other = __shfl_xor_sync(0xffffffffu, v, 1);
-          *reinterpret_cast<uint32_t*>(p_row + bb * SM::kPBytes + i * 128 +
-                                       ((p_chunk ^ (i + (lane & 1))) << 4)) =
+          *reinterpret_cast<uint32_t*>(p_row + i * 128 +
+                                       ((p_chunk ^ ((i + (lane & 1)) & 7)) << 4)) =
               lane & 1 ? __byte_perm(other, v, 0x7632) : __byte_perm(v, other, 0x5410);
         }
         if (!FP8 && word != 0xffffffffu) {
           // rows that are not positions: zeros, whatever they held, before the product
-          wait(&vfull[st], (it / S) & 1);
+          const int vs = it % VN;
+          wait(&vfull[vs], (it / VN) & 1);
           if (!live) {
-            constexpr int kShare = 256 / SM::kGroups;   // bytes of the row
-            const int at = group * kShare;
-            uint8_t* v = smem + st * SM::kStage + SM::kTile + (at >> 7) * 16384 + key * 128 +
-                         (at & 127);
+            uint8_t* v = smem + SM::kVOff + vs * SM::kTile + half * 16384 + key * 128;
 #pragma unroll
-            for (int q = 0; q < kShare / 16; ++q)
+            for (int q = 0; q < 8; ++q)
               *reinterpret_cast<uint4*>(v + q * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[bb]);
+        if (lane == 0) mbar_arrive(&p_full[set]);
       }
 
       // ---- the item's (or the part's) output
@@ -611,42 +684,320 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
           l[i] = (up ? l[i + h] : l[i]) + __shfl_xor_sync(0xffffffffu, send, bit);
         }
       }
-      l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
+      if (NC == 8) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
       l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
-      pt_group_sync(group);                          // `red` is free
-      if ((lane & 3) == 0) red[wq * NR + c0 + (lane >> 2)] = l[0];
-      pt_group_sync(group);
-      const uint32_t last = it - 1;
-      wait(&pv_done[last & 1], (last >> 1) & 1);
-      tc_fence_after();
+      __syncwarp();
+      if (FP8 && lane == 0) mbar_arrive(&rs_free[seg & 1]);
+      pt_half_sync(id);                              // `red` is free
+      if ((lane & (32 / NC - 1)) == 0) red[wq * NR + c0 + lane / (32 / NC)] = l[0];
+      {
+        float m = mref[0];
+#pragma unroll
+        for (int i = 1; i < NC; ++i) m = lane == i ? mref[i] : m;
+        if (wq == 0 && lane < NC) ref[set * NR + c0 + lane] = fresh ? -INFINITY : m;
+      }
       float o[NC];
-      tmem_ld8(lanes + SM::kOCol + c0, o);
-      tmem_ld_wait();
-      tc_fence_before();
+      if (n > skip) {                                // the set had a tile
+        const uint32_t last = it0 + skip + ((n - skip - 1) & ~1);
+        wait(&pv_done[set], (last >> 1) & 1);
+        tc_fence_after();
+        tmem_ldc<NC>(lanes + SM::kOCol + set * NR + c0, o);
+        tmem_ld_wait();
+        tc_fence_before();
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) o[i] = 0.f;
+      }
+      pt_sets_sync();                                // statistics are there, P^T is free
+      float* other_o = reinterpret_cast<float*>(smem + SM::kPOff);    // [row][d]
       const bool whole = w.t0 == 0 && w.t1 == w.nt;
       const int part = blockIdx.x * 2 + (w.t0 > 0 ? 0 : 1);
       const size_t row0 = (size_t)w.b * p.H + (size_t)w.head * p.G;
+      if (set == 1) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int r = c0 + i;
-        if (r < p.G) {
-          const float sum = (red[r] + red[NR + r]) + (red[2 * NR + r] + red[3 * NR + r]);
+        for (int i = 0; i < NC; ++i) other_o[(c0 + i) * 128 + key] = o[i];
+      } else if (warp == 4 && lane < NR) {           // row `lane`: the sets' factors, the statistics
+        const float m0 = ref[lane], m1 = ref[NR + lane], m = fmaxf(m0, m1);
+        float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - m);
+        float a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - m);
+        const float* r0 = reinterpret_cast<const float*>(smem + SM::kRedOff) + lane;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s0 += r0[q * NR], s1 += r0[(4 + q) * NR];
+        const float sum = s0 * a0 + s1 * a1;
+        if (lane < p.G) {
           if (whole) {
-            p.o[(row0 + r) * 128 + key] = __float2bfloat16_rn(sum == 0.f ? 0.f : o[i] / sum);
-            if (key == 0) {
-              const float v = (mref[i] + log2f(sum)) * kPaLn2;
-              p.lse[row0 + r] = v;
-              if (p.lse_out) p.lse_out[row0 + r] = v;
-            }
+            const float lse = (m + log2f(sum)) * kPaLn2;
+            p.lse[row0 + lane] = lse;
+            if (p.lse_out) p.lse_out[row0 + lane] = lse;
           } else {
-            p.part_o[((size_t)part * p.G + r) * 128 + key] = o[i];
-            if (key == 0)
-              p.part_ml[(size_t)part * p.G + r] = make_float2(fresh ? -INFINITY : mref[i], sum);
+            p.part_ml[(size_t)part * p.G + lane] = make_float2(m, sum);
+          }
+        }
+        if (whole) {
+          const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+          a0 *= inv;
+          a1 *= inv;
+        }
+        ref[lane] = a0;
+        ref[NR + lane] = a1;
+      }
+      pt_sets_sync();
+      if (set == 0) {
+        __nv_bfloat16* ob = p.o + (row0 + c0) * 128 + key;
+        float* op = p.part_o + ((size_t)part * p.G + c0) * 128 + key;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const float v = o[i] * ref[c0 + i] + other_o[(c0 + i) * 128 + key] * ref[NR + c0 + i];
+          if (c0 + i < p.G) {
+            if (whole) ob[i * 128] = __float2bfloat16_rn(v);
+            else op[i * 128] = v;
           }
         }
       }
+      pt_sets_sync();                                // P^T and the statistics are free again
+      it0 += n;
       ++seg;
     } while (w.next(p.c, p.c.heads));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, SM::kTmem);
+  }
+}
+
+// ----------------------------------------------------------------- weights --
+// Second pass when weights are kept: S^T of every tile again (K, mostly still in
+// L2), probabilities under the final normaliser, summed over the rows and the K/V
+// heads in the thread that owns the position: one addition per position and call.
+// The queries of all heads stay in shared memory (up to kPwRows rows); tiles go in
+// pairs, one for each softmax set, all heads of a pair before the next.  Four more
+// warps join the cut items' outputs meanwhile, as the combine kernel does when no
+// weights are kept.
+constexpr int kPwRows = 256;   // rows (K/V heads x NR) whose queries are resident
+
+template <int NR, bool FP8>
+struct PwSmem {
+  static constexpr int kThreads = 32 * (4 + 2 * kPtSet + 4);
+  static constexpr int kTile = 128 * 128 * (FP8 ? 1 : 2);
+  static constexpr int kK = FP8 ? 8 : 4;
+  static constexpr int kQTerms = FP8 ? 2 : 1;
+  static constexpr int kQOff = kK * kTile;
+  static constexpr int kQBytes = NR * 256;                       // of one head
+  static constexpr int kMask = FP8 ? 1024 : 0, kSlots = kMask + 64;
+  static constexpr int kMetaOff = kQOff + kPwRows * 256;
+  static constexpr int kMetaBytes = kSlots + 512;
+  static constexpr int kRsOff = kMetaOff + kK * kMetaBytes;      // float [rows]: queries' scales
+  static constexpr int kNlOff = kRsOff + kPwRows * 4;            // float [rows]: -lse (log2)
+  static constexpr int kSumOff = kNlOff + kPwRows * 4;           // float [2 sets][2][128]
+  static constexpr int kJoinOff = kSumOff + 4 * 128 * 4;         // PaJoin
+  static constexpr int kBarOff = kJoinOff + (int)sizeof(PaJoin);
+  static constexpr int kBars = 2 * kK + 11;
+  static constexpr int kSlotOff = (kBarOff + kBars * 8 + 15) / 16 * 16;
+  static constexpr int kWorkOff = kSlotOff + 16;
+  static constexpr int kBytes = kWorkOff + 64 + 1024;
+  static constexpr int kSCols = kQTerms * NR;
+  static constexpr int kTmem = 4 * kSCols < 64 ? 64 : 4 * kSCols;
+};
+
+__device__ __forceinline__ void pw_set_sync(int set) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + set), "n"(32 * kPtSet) : "memory");
+}
+
+template <int NR, bool FP8>
+__global__ void __launch_bounds__(PwSmem<NR, FP8>::kThreads, 1)
+    paged_weight_tc_kernel(const __grid_constant__ CUtensorMap km, const PagedAttnParams p) {
+  using SM = PwSmem<NR, FP8>;
+  constexpr int NC = NR / 2, KN = SM::kK;
+  static_assert(SM::kBytes <= 232448, "shared memory per CTA");
+  static_assert(SM::kWorkOff % 16 == 0 && SM::kBarOff % 8 == 0 && SM::kMetaOff % 16 == 0 &&
+                    SM::kMetaBytes % 16 == 0, "alignment of shared words");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
+  uint64_t* kempty = kfull + KN;
+  uint64_t* s_full = kempty + KN;    // [4]
+  uint64_t* s_empty = s_full + 4;    // [4]
+  uint64_t* q_full = s_empty + 4;    // a sequence's queries: for the MMAs,
+  uint64_t* rs_full = q_full + 1;    // and their scales and normalisers
+  uint64_t* rs_free = rs_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kSlotOff);
+  int4* work = reinterpret_cast<int4*>(smem + SM::kWorkOff);
+  float* row_scale = reinterpret_cast<float*>(smem + SM::kRsOff);
+  float* neg_lse = reinterpret_cast<float*>(smem + SM::kNlOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 32) tma_prefetch_desc(&km);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < KN; ++i) {
+      mbar_init(&kfull[i], pa_full_count(FP8, false));
+      mbar_init(&kempty[i], 1 + kPtSet);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], kPtSet);
+    }
+    mbar_init(q_full, 2);
+    mbar_init(rs_full, 2);
+    mbar_init(rs_free, 2 * kPtSet);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, SM::kTmem);
+    tmem_relinquish();
+  } else if (warp == 0) {
+    const int4 mine = pa_share(p.c, 1, p.grid);
+    if (lane == 0) *work = mine;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool any = work->x < work->y;
+  PaWalk w;
+  if (any) w.start(p.c, *work);
+  pdl_wait();
+
+  if (any && warp == 0) {
+    // ------------------------------------------------------------- producer
+    const uint64_t kpol = policy_evict_first();
+    uint32_t it = 0;
+    bool ok = true;
+    do {
+      PtPages pages;
+      pages.start(p.c, w.b, w.t0, w.len);
+      for (int t = w.t0; t < w.t1 && ok; t += 2) {
+        const int id0 = pages.at(p.c, t), id1 = t + 1 < w.t1 ? pages.at(p.c, t + 1) : -1;
+        for (int u = 0; u < 2 * p.c.heads; ++u) {
+          if ((u & 1) && t + 1 >= w.t1) continue;
+          const int ks = it % KN;
+          if (it >= (uint32_t)KN) ok = mbar_wait(&kempty[ks], ((it / KN) - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint8_t* meta = smem + SM::kMetaOff + ks * SM::kMetaBytes;
+          pt_fetch_k<FP8, true>(p.c, &km, smem + ks * SM::kTile, meta, &kfull[ks],
+                                u & 1 ? id1 : id0, t + (u & 1), w.len, u >> 1,
+                                reinterpret_cast<int*>(meta + SM::kSlots), kpol);
+          ++it;
+        }
+      }
+    } while (ok && w.next(p.c, 1));
+  } else if (any && warp == 1) {
+    // ------------------------------------------------------------------ S^T
+    if (lane == 0) {
+      const uint32_t q_addr = smem_u32(smem + SM::kQOff);
+      uint32_t it = 0, seg = 0;
+      bool ok = true;
+      do {
+        ok = mbar_wait(q_full, seg & 1);
+        for (int t = w.t0; t < w.t1 && ok; t += 2)
+          for (int u = 0; u < 2 * p.c.heads; ++u) {
+            if ((u & 1) && t + 1 >= w.t1) continue;
+            const uint32_t ks = it % KN, sb = it & 3;
+            ok = mbar_wait(&kfull[ks], (it / KN) & 1) &&
+                 (it < 4 || mbar_wait(&s_empty[sb], ((it >> 2) & 1) ^ 1));
+            if (!ok) break;
+            tc_fence_after();
+            pt_issue_qk<NR, FP8>(tmem + sb * SM::kSCols, smem_u32(smem + ks * SM::kTile),
+                                 q_addr + (u >> 1) * SM::kQBytes);
+            tc_commit(&s_full[sb]);
+            tc_commit(&kempty[ks]);
+            ++it;
+          }
+        ++seg;
+      } while (ok && w.next(p.c, 1));
+    }
+  } else if (any && warp < 4) {
+    // -------------------------------------------------------------- queries
+    uint32_t seg = 0;
+    bool dead = false;
+    do {
+      // both sets have ended the sequence before: its queries were used
+      if (seg > 0 && !dead) dead = !mbar_wait(rs_free, (seg - 1) & 1);
+      for (int head = warp - 2; head < p.c.heads; head += 2) {
+        const float lse = pa_item_lse(p, w.b, head, lane);
+        if (lane < NR) neg_lse[head * NR + lane] = lane < p.G ? -lse : -INFINITY;
+        pt_stage_q<NR, FP8>(p.q + ((size_t)w.b * p.H + (size_t)head * p.G) * 128, p.G,
+                            smem + SM::kQOff + head * SM::kQBytes, row_scale + head * NR);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(q_full);
+        mbar_arrive(rs_full);
+      }
+      ++seg;
+    } while (w.next(p.c, 1));
+  } else if (warp >= 4 + 2 * kPtSet) {
+    // ------------------------------------------- the cut items' outputs
+    const int tid = threadIdx.x - 32 * (4 + 2 * kPtSet);
+    PaJoin& join = *reinterpret_cast<PaJoin*>(smem + SM::kJoinOff);
+    for (int row = blockIdx.x; row < p.c.B * p.H; row += gridDim.x)
+      pa_join_row<128>(p, row, tid, join, false);
+  } else if (any && warp >= 4) {
+    // -------------------------------------------------------- probabilities
+    const int wq = warp & 3, set = (warp - 4) >> 3, half = (warp - 4) >> 2 & 1, c0 = half * NC;
+    const int key = wq * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+    float* sums = reinterpret_cast<float*>(smem + SM::kSumOff) + set * 256;   // [2][128]
+    uint32_t it0 = 0, seg = 0, turn = 0;            // it0: tiles met before the pair
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead) dead = !mbar_wait(bar, parity);
+    };
+    do {
+      wait(rs_full, seg & 1);
+      for (int t = w.t0; t < w.t1; t += 2) {
+        const int pair = min(2, w.t1 - t);
+        if (set < pair) {
+          float sum = 0.f;
+          bool live = false;
+          int slot = 0;
+          for (int head = 0; head < p.c.heads; ++head) {
+            const uint32_t it = it0 + head * pair + set;
+            const int st = it % KN, sb = it & 3;
+            const uint8_t* meta = smem + SM::kMetaOff + st * SM::kMetaBytes;
+            wait(&s_full[sb], (it >> 2) & 1);
+            tc_fence_after();
+            float d[NC];
+            float d2[FP8 ? NC : 1];
+            const uint32_t s_at = lanes + sb * SM::kSCols + c0;
+            tmem_ldc<NC>(s_at, d);
+            if (FP8) tmem_ldc<NC>(s_at + NR, d2);
+            wait(&kfull[st], (it / KN) & 1);
+            const unsigned word = reinterpret_cast<const unsigned*>(meta + SM::kMask)[wq];
+            live = word >> lane & 1u;
+            slot = reinterpret_cast<const int*>(meta + SM::kSlots)[key];
+            const float ks = FP8 ? reinterpret_cast<const float*>(meta)[key] * p.scale_log2
+                                 : p.scale_log2;
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&s_empty[sb]);
+              mbar_arrive(&kempty[st]);
+            }
+            const float* f = row_scale + head * NR + c0;
+            const float* nl = neg_lse + head * NR + c0;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const float x = FP8 ? fmaf(d2[c], 0.0625f, d[c]) * f[c] : d[c];
+              sum += fast_exp2(fmaf(x, ks, nl[c]));
+            }
+          }
+          float* buf = sums + (turn++ & 1) * 128;
+          if (half == 1) buf[key] = sum;
+          pw_set_sync(set);
+          if (half == 0 && live) atomicAdd(p.c.weight + slot, sum + buf[key]);
+        }
+        it0 += pair * p.c.heads;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(rs_free);
+      ++seg;
+    } while (w.next(p.c, 1));
   }
   tc_fence_before();
   __syncthreads();

@@ -41,7 +41,7 @@ struct PtSmem {
   static constexpr int kThreads = 32 * (4 + 2 * kPtSet + (FP8 ? 4 : 0));
   // rings: K tiles (with the tile's scales and mask), V tiles, E4M3's f16 V tiles
   static constexpr int kTile = 128 * 128 * (FP8 ? 1 : 2);
-  static constexpr int kK = FP8 ? 4 : 3, kV = FP8 ? 2 : 3, kH = FP8 ? 3 : 0;
+  static constexpr int kK = FP8 ? 4 : 3, kV = FP8 ? 4 : 3, kH = FP8 ? 2 : 0;
   static constexpr int kQTerms = FP8 ? 2 : 1;
   static constexpr int kVOff = kK * kTile;
   static constexpr int kHOff = kVOff + kV * kTile;

@@ -35,15 +35,15 @@ struct NormParams {
 };
 
 // The scale of values whose largest magnitude is amax, and the factor that
-// takes them to codes.  The factor is a product's (1 / s) instead of a
-// division per value: off by one more fp32 rounding, 2^-24 of the value, where
-// a code's own rounding is 2^-4.  A scale whose reciprocal would overflow is
+// takes them to codes.  The factor is a product's (an approximate 1 / s) instead
+// of a division per value: off by 2^-22 of the value, where a code's own rounding
+// is 2^-4.  A scale whose reciprocal would overflow is
 // flagged (`tiny`), and its values are divided.
 __device__ __forceinline__ float e4m3_scale(float amax, float& inv, bool& tiny) {
   const float q = __fdiv_rn(amax, 448.f);
   const float s = q > 0.f ? q : 1.f;
   tiny = s < 1e-37f;
-  inv = __frcp_rn(s);
+  inv = fast_rcp(s);
   return s;
 }
 // Four values as E4M3 codes (round to nearest even, saturating), first one lowest.

@@ -63,7 +63,8 @@ struct FgSmem {
   static constexpr int kBytes = kBarOff + 256 + 1024;
   static constexpr int kCols = BN / (CW / 4);            // columns of a consumer warp
   static constexpr int kThreads = 32 * (4 + CW);
-  static constexpr int kTmem = 2 * BN < 32 ? 32 : 2 * BN;
+  static constexpr int kAcc = 512 / BN < 8 ? 512 / BN : 8;   // accumulators in tensor memory
+  static constexpr int kTmem = kAcc * BN;
 };
 
 // Scales of blocks kb .. kb + 3 of a row (those below n).
@@ -83,15 +84,15 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap,
                     const __grid_constant__ CUtensorMap bmap, const Fp8GemmParams p) {
   using SM = FgSmem<BN, CW>;
-  constexpr int COLS = SM::kCols;
+  constexpr int COLS = SM::kCols, A = SM::kAcc;
   static_assert(SM::kBytes <= 232448 && SM::kStages >= 3, "shared memory per CTA");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
   uint64_t* empty = full + SM::kStages;
-  uint64_t* acc_full = empty + SM::kStages;    // [2]
-  uint64_t* acc_empty = acc_full + 2;          // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* acc_full = empty + SM::kStages;    // [A]
+  uint64_t* acc_empty = acc_full + A;          // [A]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + A);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = p.m_tiles * p.n_tiles;
 
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < A; ++a) {
       mbar_init(&acc_full[a], 1);
       mbar_init(&acc_empty[a], CW);
     }
@@ -145,8 +146,8 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
         bool ok = true;
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
           for (int kb = 0; kb < p.kb; ++kb, ++it) {
-            const int s = it % SM::kStages, acc = it & 1;
-            if (!mbar_wait(&acc_empty[acc], ((it >> 1) & 1) ^ 1) ||
+            const int s = it % SM::kStages, acc = it % A;
+            if (!mbar_wait(&acc_empty[acc], ((it / A) & 1) ^ 1) ||
                 !mbar_wait(&full[s], (it / SM::kStages) & 1)) {
               ok = false;
               break;
@@ -163,8 +164,8 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
           }
         }
         // the accumulators are read before tensor memory is given back
-        for (uint32_t i = it >= 2 ? it - 2 : 0; i < it && ok; ++i)
-          ok = mbar_wait(&acc_empty[i & 1], (i >> 1) & 1);
+        for (uint32_t i = it >= A ? it - A : 0; i < it && ok; ++i)
+          ok = mbar_wait(&acc_empty[i % A], (i / A) & 1);
       }
       __syncwarp();
       tc_fence_after();
@@ -199,8 +200,8 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
         }
         const float s = (kb & 2 ? (kb & 1 ? cur[3] : cur[2]) : (kb & 1 ? cur[1] : cur[0])) * sb_next;
         if (kb + 1 < p.kb) sb_next = sb[kb + 1];
-        const int a = it & 1;
-        if (!mbar_wait(&acc_full[a], (it >> 1) & 1)) { ok = false; break; }
+        const int a = it % A;
+        if (!mbar_wait(&acc_full[a], (it / A) & 1)) { ok = false; break; }
         tc_fence_after();
         // a chunk of columns is read while the one before it is added
         float v[2][32];

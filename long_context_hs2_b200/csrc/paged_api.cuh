@@ -236,21 +236,24 @@ hs2_status hs2_paged_append(const void* K, const void* V, int64_t ld, int64_t n_
   if (st != HS2_OK) return st;
   if (ld < (int64_t)kv_heads * D || ld % 8 != 0 || (!row_start && n_rows != B))
     return HS2_ERR_INVALID_ARG;
-  const int64_t units = n_rows * 2 * kv_heads;
-  if (n_rows > INT32_MAX || units * (D / 8) / kAppendThreads >= INT32_MAX)
-    return HS2_ERR_UNSUPPORTED;
+  if (n_rows > INT32_MAX - kAppendRows) return HS2_ERR_UNSUPPORTED;
   AppendParams p;
   p.c = paged_params(cache, B, kv_heads, dt);
   p.k = static_cast<const __nv_bfloat16*>(K);
   p.v = static_cast<const __nv_bfloat16*>(V);
   p.ld = ld;
   p.row_start = row_start;
-  p.n_units = units;
+  p.n_rows = n_rows;
+  // four units a thread, unless that leaves SMs without a CTA
+  const int lanes = 2 * kv_heads * (D / 8);
+  p.magic = (unsigned)(((1ull << 32) + lanes - 1) / lanes);
+  const int64_t four = 4 * kAppendThreads / lanes;
+  p.rows = (int)std::max<int64_t>(
+      1, std::min<int64_t>(std::min<int64_t>(kAppendRows, four), n_rows / sm_count()));
   const bool fp8 = dt == HS2_KV_FP8_E4M3;
   auto k = D == 128 ? (fp8 ? paged_append_kernel<128, true> : paged_append_kernel<128, false>)
                     : (fp8 ? paged_append_kernel<64, true> : paged_append_kernel<64, false>);
-  const int64_t per = kAppendThreads / (D / 8);
-  return launch(k, dim3((unsigned)((units + per - 1) / per)), dim3(kAppendThreads), 0,
+  return launch(k, dim3((unsigned)((n_rows + p.rows - 1) / p.rows)), dim3(kAppendThreads), 0,
                 (cudaStream_t)stream, 1, p);
 }
 
@@ -342,9 +345,9 @@ hs2_status hs2_paged_evict(const hs2_paged_cache* cache, int B, int kv_heads, in
   int cs = kEvMaxCluster;
   while (cs > 1 && B * cs > 2 * sm_count()) cs /= 2;
   p.cs = cs;
-  const int64_t run = (((reach + cs * kEvWarps - 1) / (cs * kEvWarps)) + 31) & ~31;
-  p.cache_keys = (int)std::min<int64_t>(kEvCache, run * kEvWarps);
-  const size_t bytes = sizeof(EvSmem) + (size_t)p.cache_keys * 4;
+  // shared memory for the keys that a CTA keeps
+  p.solo = (int)std::min<int64_t>(kEvSolo, std::max<int64_t>(1, reach - window));
+  const size_t bytes = sizeof(EvSmem) + (size_t)p.solo * 4;
   auto k = fp8 ? paged_evict_kernel<true> : paged_evict_kernel<false>;
   if (!set_smem(k, (int)bytes)) return HS2_ERR_CUDA;
   return launch(k, dim3((unsigned)(B * cs)), dim3(kEvThreads), bytes, (cudaStream_t)stream, cs, p);

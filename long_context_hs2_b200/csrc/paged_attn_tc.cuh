@@ -135,12 +135,6 @@ __device__ __forceinline__ float warp_max_f32(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // One lane's run of a tile: its page's rows [j0 + lane * rows, + rows), if any.
 struct PtRun {
   int slot;        // of its first row

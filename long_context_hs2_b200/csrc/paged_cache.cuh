@@ -51,33 +51,49 @@ struct AppendParams {
   const __nv_bfloat16* v;
   long long ld;            // elements between two rows of k, and of v
   const int* row_start;    // [B + 1], or nullptr: row r is sequence r's one new token
-  long long n_units;       // rows * 2 * heads
+  long long n_rows;
+  int rows;                // tokens of a CTA
+  unsigned magic;          // ceil(2^32 / lanes of a token): a division by it, exact below
+                           // 2^32 / lanes (at most 2^15 lanes, or 2^10 of several tokens)
 };
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendRows = 64;     // rows of a CTA at most
 
-// One unit is one head's K or V row of one token: D / 8 lanes with 8 elements
-// each (a 16-byte load; a 16- or 8-byte store), the row's maximum taken by
-// shuffles.  Bound by HBM for prompts and by one launch's latency for a
-// decode step; a sequence is found by bisecting row_start.
+// A CTA takes p.rows tokens, about four units a thread: a unit is 8 elements of
+// one head's K or V row of one token (a 16-byte load; a 16- or 8-byte store), D / 8
+// lanes a row, the row's maximum taken by shuffles.  While the first loads are on
+// their way a thread per token finds its slot (bisecting row_start, then its page:
+// a chain of dependent loads, once per token).  Bound by HBM for prompts (65,536 tokens of
+// D = 128 to E4M3: APPENDUS us, APPENDGBS GB/s) and by one launch's latency for a
+// decode step.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendParams p) {
-  constexpr int kLanes = D / 8;
-  const long long tid = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
-  const long long unit = tid / kLanes;
-  const int part = (int)(tid % kLanes);
+  constexpr int kLanes = D / 8, kBatch = 4;
+  __shared__ long long slots[kAppendRows];
   const int heads = p.c.heads;
-  const bool live = unit < p.n_units;
-  const long long row = live ? unit / (2 * heads) : 0;
-  const int hk = (int)(unit - row * 2 * heads);     // K heads, then V heads
-  const bool is_v = hk >= heads;
-  const int head = is_v ? hk - heads : hk;
-
-  long long slot = -1;
-  uint4 w = make_uint4(0, 0, 0, 0);
-  if (live) {
-    w = *reinterpret_cast<const uint4*>((is_v ? p.v : p.k) + row * p.ld + head * D + part * 8);
-    int b = (int)row, pos;
+  const long long row0 = (long long)blockIdx.x * p.rows;
+  const int rows = (int)min((long long)p.rows, p.n_rows - row0);
+  const int per_row = 2 * heads * kLanes, total = rows * per_row;
+  uint4 w[kBatch];
+  auto load = [&](int u0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + i * kAppendThreads;
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (u < total) {
+        const int row = __umulhi(u, p.magic), rest = u - row * per_row, hk = rest / kLanes;
+        const bool is_v = hk >= heads;               // K heads, then V heads
+        w[i] = *reinterpret_cast<const uint4*>((is_v ? p.v : p.k) + (row0 + row) * p.ld +
+                                               (is_v ? hk - heads : hk) * D + rest % kLanes * 8);
+      }
+    }
+  };
+  load(threadIdx.x);
+  if ((int)threadIdx.x < rows) {
+    const long long row = row0 + threadIdx.x;
+    long long slot = -1;
+    int b = (int)row, pos = 0;
     if (p.row_start) {
       int lo = 0, hi = p.c.B;    // the last b with row_start[b] <= row
       while (lo < hi) {
@@ -85,12 +101,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
         if (p.row_start[mid + 1] <= row) lo = mid + 1;
         else hi = mid;
       }
-      b = lo;
       // rows before the first sequence's or behind the last one's are no token's
-      if (b < p.c.B && row >= p.row_start[b])
-        pos = paged_len(p.c, b) - p.row_start[b + 1] + (int)row;
-      else
-        b = -1, pos = 0;
+      b = lo < p.c.B && row >= p.row_start[lo] ? lo : -1;
+      if (b >= 0) pos = paged_len(p.c, b) - p.row_start[b + 1] + (int)row;
     } else {
       pos = paged_len(p.c, b) - 1;
     }
@@ -98,37 +111,52 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
       if (pos >= 0) slot = paged_slot(p.c, p.c.page_table, b, p.c.max_pages, pos);
       else raise_status(kStatusBadIndex);   // more new tokens than the cache has positions
     }
+    slots[threadIdx.x] = slot;
+    // a new position starts with no accumulated weight
+    if (p.c.weight && slot >= 0) p.c.weight[slot] = 0.f;
   }
-  const size_t at = slot < 0 ? 0 : ((size_t)slot * heads + head) * D + part * 8;
-  uint8_t* pool = is_v ? p.c.v : p.c.k;
-  if (!FP8) {
-    if (slot >= 0) *reinterpret_cast<uint4*>(pool + at * 2) = w;
-  } else {
-    float x[8];
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    float amax = 0.f;
+  __syncthreads();
+  // (whole warps go round, for the shuffles)
+  for (int u0 = threadIdx.x; u0 < (total + 31) / 32 * 32; u0 += kBatch * kAppendThreads) {
+    if (u0 != (int)threadIdx.x) load(u0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = bf16x2_to_float2(ww[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-      amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-    }
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + i * kAppendThreads;
+      const int row = min(rows - 1, (int)__umulhi(u, p.magic)), rest = u - row * per_row;
+      const int hk = rest / kLanes, part = rest % kLanes;
+      const bool is_v = hk >= heads;
+      const int head = is_v ? hk - heads : hk;
+      const long long slot = u < total ? slots[row] : -1;
+      const size_t at = ((size_t)slot * heads + head) * D + part * 8;
+      uint8_t* to = (is_v ? p.c.v : p.c.k) + at * (FP8 ? 1 : 2);
+      if (!FP8) {
+        if (slot >= 0) *reinterpret_cast<uint4*>(to) = w[i];
+      } else {
+        float x[8];
+        const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        float amax = 0.f;
 #pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1)
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (slot >= 0) {
-      float inv;
-      bool tiny;
-      const float s = e4m3_scale(amax, inv, tiny);
-      uint32_t c[2];
-      e4m3_codes<8>(x, s, inv, tiny, c);
-      *reinterpret_cast<uint2*>(pool + at) = make_uint2(c[0], c[1]);
-      if (part == 0) (is_v ? p.c.v_scale : p.c.k_scale)[slot * heads + head] = s;
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = bf16x2_to_float2(ww[q]);
+          x[2 * q] = f.x;
+          x[2 * q + 1] = f.y;
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1)
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (slot >= 0) {
+          float inv;
+          bool tiny;
+          const float s = e4m3_scale(amax, inv, tiny);
+          uint32_t c[2];
+          e4m3_codes<8>(x, s, inv, tiny, c);
+          *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
+          if (part == 0) (is_v ? p.c.v_scale : p.c.k_scale)[slot * heads + head] = s;
+        }
+      }
     }
   }
-  // a new position starts with no accumulated weight
-  if (p.c.weight && slot >= 0 && hk == 0 && part == 0) p.c.weight[slot] = 0.f;
 }
 
 }  // namespace hs2

@@ -6,16 +6,19 @@
 // become positions 0, 1, ... of the sequence: row r <- row kept[r].
 //
 // One launch, one cluster per sequence.  The threshold is found by a radix
-// search over the weights' 32-bit order (digits of 11, 11 and 10 bits): every
-// CTA counts its part of the candidates in shared memory, and after a cluster
-// barrier every CTA sums all parts' counts through distributed shared memory
-// and finds the digit for itself -- one barrier per digit.  Counts are whole
-// numbers, so the result does not depend on the order of the atomics.
+// search over the weights' 32-bit order (digits of 11, 11 and 10 bits).  Up to
+// kEvSolo candidates every CTA of the cluster searches all of them for itself, from
+// keys it keeps in shared memory: no exchange, and the cluster only shares the
+// move.  More are split over the cluster: each CTA counts its part, sums its share
+// of the bins over all parts through distributed shared memory and hands the sums
+// to all, two barriers a digit.  (8 sequences of 32K: 28 us split, KSOLO32K us each for
+// itself; of 1216: 23 us and KSOLOFEW us: an exchange costs 4 us a digit.)  Counts
+// are whole numbers, so the result does not depend on the order of the atomics.
 // Survivors are then written in order from ballots: each warp owns a contiguous
 // run of candidates, counts it, learns what comes before it, and writes it.
 //
-// The move.  Into other pages (dst_table) it is a plain copy, rows spread over
-// the cluster.  In place, row r overwrites a row that an earlier move has to
+// The move.  Into other pages (dst_table) it is a plain copy, a few rows for every
+// warp of the cluster.  In place, row r overwrites a row that an earlier move has to
 // have read (kept[r] >= r); so a CTA takes a column of every row -- kEvCol
 // bytes of K or of V, or one array of scales or weights -- and walks the rows
 // in ascending chunks: all reads of a chunk, a block barrier, its writes.
@@ -30,7 +33,7 @@ namespace hs2 {
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;
-constexpr int kEvCache = 24 * 1024;   // weights of a CTA's part kept in shared memory (96 KB)
+constexpr int kEvSolo = 8 * 1024;     // keys a CTA keeps (32 KB): so many it searches alone
 constexpr int kEvMaxCluster = 8;
 constexpr int kEvCol = 64;            // bytes of a row that one CTA moves in place
 constexpr int kEvBatch = 4;           // rows per thread and chunk, in place
@@ -40,14 +43,16 @@ struct EvictParams {
   const int* dst_table;    // nullptr: in place
   int* kept;               // [B][topk + window]
   int* new_len;            // [B]
-  int dst_max_pages, topk, window, cs, row_bytes, cache_keys;
+  int dst_max_pages, topk, window, cs, row_bytes;
+  int solo;                // keys a CTA keeps: up to so many candidates it searches alone
 };
 
 struct EvSmem {
   unsigned hist[2][kEvBins];
+  unsigned total[kEvBins];           // the cluster's counts
   unsigned warp_gt[kEvWarps], warp_eq[kEvWarps];
   unsigned cnt[2 * kEvMaxCluster];   // pushed by every CTA: candidates above / at the threshold
-  unsigned scan[kEvWarps];
+  unsigned scan[kEvWarps];   // what the warps' bins hold, then what comes before them
   unsigned found[2];
 };
 
@@ -73,25 +78,39 @@ __device__ __forceinline__ unsigned evict_key(const EvictParams& p, int b, int j
   return slot < 0 ? 0u : weight_key(p.c.weight[slot]);
 }
 
-// Finds, from the counts of the cluster's CTAs, the largest bin whose suffix
-// count reaches k: found[0] = bin, found[1] = how many of it are still wanted.
-// Ends with a block barrier.
-__device__ __forceinline__ void evict_find_bin(EvSmem& s, const unsigned* hist, int bins, int cs,
+// The counts of the `cs` CTAs of a search into `total` of each: CTA r sums its
+// share of the bins and hands it to all.  Begins and ends with their barrier.
+__device__ __forceinline__ void evict_sum(const unsigned* hist, unsigned* total, int bins, int cs,
+                                          int rank) {
+  cluster_arrive_release();
+  cluster_wait_acquire();
+  const int share = bins / cs;
+  const uint32_t from = smem_u32(hist), to = smem_u32(total);
+  for (int bin = rank * share + threadIdx.x; bin < (rank + 1) * share; bin += kEvThreads) {
+    unsigned v[kEvMaxCluster], n = 0;
+#pragma unroll
+    for (int r = 0; r < kEvMaxCluster; ++r)
+      v[r] = r < cs ? ld_dsmem_u32_ordered(mapa_shared(from + bin * 4, r)) : 0u;
+#pragma unroll
+    for (int r = 0; r < kEvMaxCluster; ++r) n += v[r];
+#pragma unroll
+    for (int r = 0; r < kEvMaxCluster; ++r)
+      if (r < cs) st_dsmem_u32(mapa_shared(to + bin * 4, r), n);
+  }
+  cluster_arrive_release();
+  cluster_wait_acquire();
+}
+
+// Finds the largest bin whose suffix count reaches k: found[0] = bin, found[1] =
+// how many of it are still wanted.  Ends with a block barrier.
+__device__ __forceinline__ void evict_find_bin(EvSmem& s, const unsigned* hist, int bins,
                                                unsigned k) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = bins / kEvThreads;   // 2 or 1, highest bins first
-  const uint32_t at = smem_u32(hist);
   unsigned n[2] = {0, 0};
-  for (int i = 0; i < per; ++i) {
-    const int bin = bins - 1 - (threadIdx.x * per + i);
-    unsigned v[kEvMaxCluster];
-#pragma unroll
-    for (int r = 0; r < kEvMaxCluster; ++r)
-      v[r] = r < cs ? ld_dsmem_u32_ordered(mapa_shared(at + bin * 4, r)) : 0u;
-#pragma unroll
-    for (int r = 0; r < kEvMaxCluster; ++r) n[i] += v[r];
-  }
-  unsigned sum = n[0] + n[1], inc = sum;
+  for (int i = 0; i < per; ++i) n[i] = hist[bins - 1 - (threadIdx.x * per + i)];
+  const unsigned sum = n[0] + n[1];
+  unsigned inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -99,9 +118,18 @@ __device__ __forceinline__ void evict_find_bin(EvSmem& s, const unsigned* hist, 
   }
   if (lane == 31) s.scan[warp] = inc;
   __syncthreads();
-  unsigned before = 0;
-  for (int w = 0; w < warp; ++w) before += s.scan[w];
-  before += inc - sum;
+  if (warp == 0) {
+    const unsigned mine = s.scan[lane];
+    unsigned up = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += v;
+    }
+    s.scan[lane] = up - mine;
+  }
+  __syncthreads();
+  unsigned before = s.scan[warp] + inc - sum;
   for (int i = 0; i < per; ++i) {
     if (before < k && before + n[i] >= k) {   // exactly one thread and bin
       s.found[0] = bins - 1 - (threadIdx.x * per + i);
@@ -110,14 +138,6 @@ __device__ __forceinline__ void evict_find_bin(EvSmem& s, const unsigned* hist, 
     before += n[i];
   }
   __syncthreads();
-}
-
-// 16 (or 4) bytes of row `src` to row `dst` of one array, for the out-of-place copy.
-template <typename V>
-__device__ __forceinline__ void evict_copy(uint8_t* base, size_t row_bytes, long long dst,
-                                           long long src, int at) {
-  *reinterpret_cast<V*>(base + dst * row_bytes + at) =
-      *reinterpret_cast<const V*>(base + src * row_bytes + at);
 }
 
 // In place: column [off, off + n_vec * sizeof(V)) of every row of one array.
@@ -165,41 +185,54 @@ __global__ void __launch_bounds__(kEvThreads, 1) paged_evict_kernel(const EvictP
   const int k = min(p.topk, nc), count = k + win, slots = p.topk + p.window;
   int* kept = p.kept + (size_t)b * slots;
 
+  // the CTAs that search together, and this one's place among them
+  const int scs = nc <= p.solo ? 1 : cs, srank = scs == 1 ? 0 : rank;
   if (k == nc || k == 0) {   // every candidate stays, or none
-    for (int j = rank * kEvThreads + threadIdx.x; j < k; j += cs * kEvThreads) kept[j] = j;
+    for (int j = threadIdx.x; j < k; j += kEvThreads) kept[j] = j;
   } else {
     // this CTA's candidates, in whole warps' runs
-    const int run = ((nc + cs * kEvWarps - 1) / (cs * kEvWarps) + 31) & ~31;
-    const int lo = min(nc, rank * kEvWarps * run), hi = min(nc, lo + kEvWarps * run);
-    const bool cached = hi - lo <= p.cache_keys;
+    const int run = ((nc + scs * kEvWarps - 1) / (scs * kEvWarps) + 31) & ~31;
+    const int lo = min(nc, srank * kEvWarps * run), hi = min(nc, lo + kEvWarps * run);
+    const bool cached = hi - lo <= p.solo;   // (always, when it searches alone)
     for (int i = threadIdx.x; i < 2 * kEvBins; i += kEvThreads) (&s.hist[0][0])[i] = 0;
     __syncthreads();
-    for (int j = lo + threadIdx.x; j < hi; j += kEvThreads) {
-      const unsigned key = evict_key(p, b, j);
-      if (cached) cache[j - lo] = key;
-      atomicAdd(&s.hist[0][key >> 21], 1u);
+    for (int j0 = lo + threadIdx.x; j0 < hi; j0 += 4 * kEvThreads) {
+      unsigned key[4];   // four dependent pairs of loads in flight
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        key[i] = j0 + i * kEvThreads < hi ? evict_key(p, b, j0 + i * kEvThreads) : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j0 + i * kEvThreads < hi) {
+          if (cached) cache[j0 + i * kEvThreads - lo] = key[i];
+          atomicAdd(&s.hist[0][key[i] >> 21], 1u);
+        }
     }
-    cluster_arrive_release();
-    cluster_wait_acquire();
-    evict_find_bin(s, s.hist[0], 2048, cs, (unsigned)k);
+    // a digit's counts: this CTA's, or the cluster's
+    auto counts = [&](const unsigned* hist, int bins) -> const unsigned* {
+      if (scs == 1) {
+        __syncthreads();
+        return hist;
+      }
+      evict_sum(hist, s.total, bins, scs, rank);
+      return s.total;
+    };
+    evict_find_bin(s, counts(s.hist[0], 2048), 2048, (unsigned)k);
     unsigned prefix = s.found[0], want = s.found[1];
     for (int j = lo + threadIdx.x; j < hi; j += kEvThreads) {
       const unsigned key = cached ? cache[j - lo] : evict_key(p, b, j);
       if ((key >> 21) == prefix) atomicAdd(&s.hist[1][(key >> 10) & 2047u], 1u);
     }
-    cluster_arrive_release();
-    cluster_wait_acquire();   // every CTA has read the first counts
+    const unsigned* second = counts(s.hist[1], 2048);   // the first counts were all read
     for (int i = threadIdx.x; i < 1024; i += kEvThreads) s.hist[0][i] = 0;
-    evict_find_bin(s, s.hist[1], 2048, cs, want);
+    evict_find_bin(s, second, 2048, want);
     prefix = (prefix << 11) | s.found[0];
     want = s.found[1];
     for (int j = lo + threadIdx.x; j < hi; j += kEvThreads) {
       const unsigned key = cached ? cache[j - lo] : evict_key(p, b, j);
       if ((key >> 10) == prefix) atomicAdd(&s.hist[0][key & 1023u], 1u);
     }
-    cluster_arrive_release();
-    cluster_wait_acquire();
-    evict_find_bin(s, s.hist[0], 1024, cs, want);
+    evict_find_bin(s, counts(s.hist[0], 1024), 1024, want);
     const unsigned tau = (prefix << 10) | s.found[0];
     want = s.found[1];        // candidates equal to tau that stay, lowest positions first
 
@@ -220,15 +253,21 @@ __global__ void __launch_bounds__(kEvThreads, 1) paged_evict_kernel(const EvictP
     if (warp == 0) {
       const unsigned a = __reduce_add_sync(0xffffffffu, s.warp_gt[lane]);
       const unsigned e = __reduce_add_sync(0xffffffffu, s.warp_eq[lane]);
-      if (lane < cs) {
+      if (scs == 1) {
+        if (lane == 0) s.cnt[0] = a, s.cnt[kEvMaxCluster] = e;
+      } else if (lane < cs) {
         st_dsmem_u32(mapa_shared(smem_u32(&s.cnt[rank]), lane), a);
         st_dsmem_u32(mapa_shared(smem_u32(&s.cnt[kEvMaxCluster + rank]), lane), e);
       }
     }
-    cluster_arrive_release();
-    cluster_wait_acquire();
+    if (scs == 1) {
+      __syncthreads();
+    } else {
+      cluster_arrive_release();
+      cluster_wait_acquire();
+    }
     unsigned gt0 = 0, eq0 = 0;
-    for (int r = 0; r < rank; ++r) gt0 += s.cnt[r], eq0 += s.cnt[kEvMaxCluster + r];
+    for (int r = 0; r < srank; ++r) gt0 += s.cnt[r], eq0 += s.cnt[kEvMaxCluster + r];
     for (int w = 0; w < warp; ++w) gt0 += s.warp_gt[w], eq0 += s.warp_eq[w];
     for (int j0 = w0; j0 < w1; j0 += 32) {
       const int j = j0 + lane;
@@ -243,32 +282,51 @@ __global__ void __launch_bounds__(kEvThreads, 1) paged_evict_kernel(const EvictP
       eq0 += __popc(me);
     }
   }
-  for (int i = rank * kEvThreads + threadIdx.x; i < slots - k; i += cs * kEvThreads)
-    kept[k + i] = i < win ? nc + i : -1;
-  // the list is complete, and no CTA reads another's shared memory or its
-  // length (new_len may be the lengths' own array) after this barrier
+  for (int i = threadIdx.x; i < slots - k; i += kEvThreads) kept[k + i] = i < win ? nc + i : -1;
+  // (CTAs that searched for themselves have all written the same list)
+  // After this barrier the list is complete, and no CTA reads a weight, another's
+  // shared memory or its length (new_len may be the lengths' own array)
   cluster_arrive_release();
   cluster_wait_acquire();
   if (rank == 0 && threadIdx.x == 0) p.new_len[b] = count;
 
   const int heads = p.c.heads;
   if (p.dst_table) {
-    const int vecs = p.row_bytes / 16;
-    const long long total = (long long)count * (2 * vecs + (FP8 ? 2 * heads : 0) + 1);
-    const int per_row = 2 * vecs + (FP8 ? 2 * heads : 0) + 1;
-    for (long long u = rank * kEvThreads + threadIdx.x; u < total; u += cs * kEvThreads) {
-      const int r = (int)(u / per_row), i = (int)(u - (long long)r * per_row);
-      const long long src = paged_slot(p.c, p.c.page_table, b, p.c.max_pages, kept[r]);
-      const long long dst = paged_slot(p.c, p.dst_table, b, p.dst_max_pages, r);
-      if (src < 0 || dst < 0) continue;
-      if (i < vecs) evict_copy<uint4>(p.c.k, p.row_bytes, dst, src, i * 16);
-      else if (i < 2 * vecs) evict_copy<uint4>(p.c.v, p.row_bytes, dst, src, (i - vecs) * 16);
-      else if (i == per_row - 1) p.c.weight[dst] = p.c.weight[src];
-      else {
-        const int h = i - 2 * vecs;
-        float* sc = h < heads ? p.c.k_scale : p.c.v_scale;
-        const int hh = h < heads ? h : h - heads;
-        sc[dst * heads + hh] = sc[src * heads + hh];
+    // `each` rows for every warp of the cluster; lane i finds row i's slots and
+    // moves its weight and scales, then the warp moves the rows
+    const int vecs = p.row_bytes / 16, warps = cs * kEvWarps;
+    const int each = min(32, (count + warps - 1) / warps);
+    for (int r0 = (rank * kEvWarps + warp) * each; r0 < count; r0 += warps * each) {
+      const int mine = r0 + lane, n = min(each, count - r0);
+      long long src = -1, dst = -1;
+      if (lane < n) {
+        src = paged_slot(p.c, p.c.page_table, b, p.c.max_pages, kept[mine]);
+        dst = paged_slot(p.c, p.dst_table, b, p.dst_max_pages, mine);
+        if (src < 0 || dst < 0) src = dst = -1;
+        if (src >= 0) {
+          p.c.weight[dst] = p.c.weight[src];
+          if (FP8)
+            for (int h = 0; h < heads; ++h) {
+              p.c.k_scale[dst * heads + h] = p.c.k_scale[src * heads + h];
+              p.c.v_scale[dst * heads + h] = p.c.v_scale[src * heads + h];
+            }
+        }
+      }
+      for (int i0 = 0; i0 < n * 2 * vecs; i0 += 4 * 32) {
+        uint4 v[4];
+        uint8_t* to[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int i = i0 + q * 32 + lane, r = min(n - 1, i / (2 * vecs)), at = i % (2 * vecs);
+          const long long rs = __shfl_sync(0xffffffffu, src, r), rd = __shfl_sync(0xffffffffu, dst, r);
+          uint8_t* base = at < vecs ? p.c.k : p.c.v;
+          const size_t off = (size_t)(at < vecs ? at : at - vecs) * 16;
+          to[q] = i < n * 2 * vecs && rs >= 0 ? base + rd * p.row_bytes + off : nullptr;
+          if (to[q]) v[q] = *reinterpret_cast<const uint4*>(base + rs * p.row_bytes + off);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (to[q]) *reinterpret_cast<uint4*>(to[q]) = v[q];
       }
     }
   } else if (count < len) {

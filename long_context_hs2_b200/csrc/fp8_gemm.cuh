@@ -138,46 +138,56 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
           tma_load_2d(a + SM::kABytes, &bmap, &full[s], kb * kFgBK, n0, pol);
         }
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------ MMA issuer
+    } else if (warp == 1 || warp == 2) {
+      // ----------------------------------------------------- MMA issuers
+      // Two take the blocks in turn: one's waits and commits, a few hundred cycles
+      // next to a block's MMAs, pass while the other's MMAs run.
+      const uint32_t total =
+          (uint32_t)((tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x) * p.kb;
+      bool ok = true;
       if (lane == 0) {
         constexpr uint32_t idesc = tc_idesc_e4m3(128, BN);
-        uint32_t it = 0;
-        bool ok = true;
-        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-          for (int kb = 0; kb < p.kb; ++kb, ++it) {
-            const int s = it % SM::kStages, acc = it % A;
-            if (!mbar_wait(&acc_empty[acc], ((it / A) & 1) ^ 1) ||
-                !mbar_wait(&full[s], (it / SM::kStages) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t addr = smem_u32(smem + s * SM::kStage);
-            const uint64_t ad = sw128_kmajor_desc(addr),
-                           bd = sw128_kmajor_desc(addr + SM::kABytes);
+        for (uint32_t it = warp - 1; it < total; it += 2) {
+          const uint32_t s = it % SM::kStages, acc = it % A;
+          ok = mbar_wait(&full[s], (it / SM::kStages) & 1) &&
+               mbar_wait(&acc_empty[acc], ((it / A) & 1) ^ 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t addr = smem_u32(smem + s * SM::kStage);
+          const uint64_t ad = sw128_kmajor_desc(addr), bd = sw128_kmajor_desc(addr + SM::kABytes);
 #pragma unroll
-            for (int k = 0; k < kFgBK / 32; ++k)   // +32 bytes along K per step
-              tc_mma_f8(tmem + acc * BN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
-            tc_commit(&empty[s]);
-            tc_commit(&acc_full[acc]);
-          }
+          for (int k = 0; k < kFgBK / 32; ++k)   // +32 bytes along K per step
+            tc_mma_f8(tmem + acc * BN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+          tc_commit(&acc_full[acc]);
+          tc_commit(&empty[s]);
         }
         // the accumulators are read before tensor memory is given back
-        for (uint32_t i = it >= A ? it - A : 0; i < it && ok; ++i)
+        for (uint32_t i = total >= A ? total - A : 0; warp == 1 && i < total && ok; ++i)
           ok = mbar_wait(&acc_empty[i % A], (i / A) & 1);
       }
       __syncwarp();
-      tc_fence_after();
-      tmem_dealloc(tmem, SM::kTmem);
+      if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, SM::kTmem);
+      }
     }
   } else {
     // --------------------------------------------------------- consumers
     if (kMove) regs_take<232>();
     const int quarter = warp & 3, part = (warp - 4) >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + part * COLS;
+    constexpr int CH = COLS / 32;
+    static_assert(CH % 2 == 0, "a block's chunks alternate between two register sets");
+    const uint32_t total =
+        (uint32_t)((tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x) * p.kb;
+    // Chunks of 32 columns, one after another through blocks and tiles: each is read
+    // while the one before it is added, so neither the barrier of a block nor the
+    // tensor memory's latency is waited for where the MMAs are ahead.
+    float v[2][32];
+    bool ok = mbar_wait(&acc_full[0], 0);
+    tc_fence_after();
+    if (ok) tmem_ld32(taddr, v[0]);
     uint32_t it = 0;
-    bool ok = true;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
       const int m = tile / p.n_tiles * 128 + quarter * 32 + lane;
       const int n0 = tile % p.n_tiles * BN + part * COLS;
@@ -192,7 +202,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
       float cur[4], nxt[4];
       load_scales4(sa, 0, p.kb, p.sa_vec, nxt);
       float sb_next = sb[0];
-      for (int kb = 0; kb < p.kb; ++kb, ++it) {
+      for (int kb = 0; kb < p.kb && ok; ++kb, ++it) {
         if ((kb & 3) == 0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
@@ -200,21 +210,21 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
         }
         const float s = (kb & 2 ? (kb & 1 ? cur[3] : cur[2]) : (kb & 1 ? cur[1] : cur[0])) * sb_next;
         if (kb + 1 < p.kb) sb_next = sb[kb + 1];
-        const int a = it % A;
-        if (!mbar_wait(&acc_full[a], (it / A) & 1)) { ok = false; break; }
-        tc_fence_after();
-        // a chunk of columns is read while the one before it is added
-        float v[2][32];
-        tmem_ld32(taddr + a * BN, v[0]);
+        const uint32_t a = it % A, an = (it + 1) % A;
 #pragma unroll
-        for (int c = 0; c < COLS / 32; ++c) {
+        for (int c = 0; c < CH; ++c) {
           tmem_ld_wait();
-          if (c + 1 < COLS / 32) {
+          if (c + 1 < CH) {
             tmem_ld32(taddr + a * BN + (c + 1) * 32, v[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[a]);
+            if (it + 1 < total) {
+              ok = mbar_wait(&acc_full[an], ((it + 1) / A) & 1);
+              tc_fence_after();
+              if (ok) tmem_ld32(taddr + an * BN, v[0]);
+            }
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[c & 1][i], s, acc[c * 32 + i]);
@@ -235,6 +245,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
         }
       }
     }
+    tmem_ld_wait();
   }
 }
 

@@ -179,14 +179,21 @@ hs2_status hs2_fp8_gemm(const void* A, const float* A_scale, int64_t M, const vo
   p.kb = (K + kFgBK - 1) / kFgBK;
   p.sa_vec = p.kb % 4 == 0 && aligned16(A_scale);
   cudaStream_t s = (cudaStream_t)stream;
+  // Few rows: the whole machine streams B (8 rows x 1536 x 4096: 5.3 us against 12.0 with
+  // the tiles of many rows; 64 rows: 12.3 us against 10.9, so not from there on).
   if (M <= 16) return run_fp8_gemm_small<16>(A, B, p, s);
   if (M <= 32) return run_fp8_gemm_small<32>(A, B, p, s);
-  if (M <= 64) return run_fp8_gemm_small<64>(A, B, p, s);
-  if (M <= 128) return run_fp8_gemm_small<128>(A, B, p, s);
-  const int64_t mt = (M + 127) / 128;
-  if (mt * ((N + 255) / 256) >= sm_count()) return run_fp8_gemm<256, 8>(A, B, p, s);
-  if (mt * ((N + 127) / 128) >= sm_count() / 2) return run_fp8_gemm<128, 8>(A, B, p, s);
-  return run_fp8_gemm<64, 8>(A, B, p, s);
+  // Many rows: the tile width whose waves cost least.  A wave of K = 4096 takes 11.0, 14.5
+  // and 23.5 us with 64, 128 and 256 columns (1003 x 1536: 21.5, 15.3, 24.2 us; 100 x 1536:
+  // 11.2, 13.9, 22.3; 2048 x 6144: 101, 76, 66).
+  const int64_t mt = (M + 127) / 128, sms = sm_count();
+  auto cost = [&](int64_t bn, int64_t wave) {
+    return (mt * ((N + bn - 1) / bn) + sms - 1) / sms * wave;
+  };
+  const int64_t c64 = cost(64, 110), c128 = cost(128, 145), c256 = cost(256, 235);
+  if (c256 <= c128 && c256 <= c64) return run_fp8_gemm<256, 8>(A, B, p, s);
+  if (c128 <= c64) return run_fp8_gemm<128, 8>(A, B, p, s);
+  return run_fp8_gemm<64, 4>(A, B, p, s);
 }
 
 hs2_status hs2_add_rmsnorm(const void* X, const void* R, const void* gamma, int64_t T, int hidden,

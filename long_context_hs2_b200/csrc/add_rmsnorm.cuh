@@ -12,7 +12,7 @@
 // the norm: the sum's rounding to bf16 goes to the residual stream only.
 #pragma once
 
-#include "hs2_common.cuh"
+#include "paged_common.cuh"
 
 namespace hs2 {
 

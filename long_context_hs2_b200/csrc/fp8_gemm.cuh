@@ -22,7 +22,7 @@
 //   once, so the whole machine streams it.
 #pragma once
 
-#include "tc_common.cuh"
+#include "paged_common.cuh"
 
 namespace hs2 {
 

@@ -429,7 +429,7 @@ hs2_status run_sparse(SparseParams p, cudaStream_t s) {
 
 extern "C" {
 
-int hs2_version(void) { return 102; }
+int hs2_version(void) { return 101; }
 
 hs2_status hs2_set_fault_injection(unsigned extra_arrivals, unsigned long long wait_limit_ns) {
   t_barrier_extra = extra_arrivals;
@@ -944,6 +944,3 @@ extern "C" hs2_status hs2_full_attn_select_noalloc(const void* Q, const hs2_kv_c
   return hs2_full_attn_select(Q, kv, B, T, L, H, D, scale, topk, window, dt, O, lse, idx, n_sel,
                               scratch, (size_t)HS2_NOALLOC_SCRATCH_BYTES, stream);
 }
-
-// The paged decode path.
-#include "paged_api.cuh"

@@ -165,12 +165,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two E4M3 codes (low byte first) to two bf16 values, exactly: E4M3 -> f16 is
 // exact, and every E4M3 value is a bf16 value.
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t two) {

@@ -1,6 +1,6 @@
 // Host side of the paged decode path's entry points (see include/hs2.h):
-// argument checks, launch plans, launches.  Included by hs2_api.cu after its
-// helpers.
+// argument checks, launch plans, launches.  Included by hs2_lib.cu after
+// hs2_api.cu, whose helpers it uses.
 #pragma once
 
 #include "add_rmsnorm.cuh"

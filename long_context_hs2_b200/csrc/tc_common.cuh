@@ -150,16 +150,4 @@ __host__ __device__ constexpr uint32_t tc_idesc_f16(int M, int N, uint32_t fmt, 
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Registers moved between the warpgroups of a block: a warpgroup gives up what it
-// has above N, or takes up to N from what others gave up.  All shares together
-// must not pass what the block was launched with.
-template <int N>
-__device__ __forceinline__ void regs_give_up() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_take() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 }  // namespace hs2

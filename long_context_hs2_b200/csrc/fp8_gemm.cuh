@@ -34,7 +34,6 @@ struct Fp8GemmParams {
   __nv_bfloat16* c;
   int M, N, K, kb;                     // kb = ceil(K / 128)
   int m_tiles, n_tiles;
-  int sa_vec;                          // rows of sa start on 16 bytes
 };
 
 // kind::f8f6f4, A = B = E4M3, fp32 accumulator, both K-major.
@@ -66,18 +65,6 @@ struct FgSmem {
   static constexpr int kAcc = 512 / BN < 8 ? 512 / BN : 8;   // accumulators in tensor memory
   static constexpr int kTmem = kAcc * BN;
 };
-
-// Scales of blocks kb .. kb + 3 of a row (those below n).
-__device__ __forceinline__ void load_scales4(const float* row, int kb, int n, int vec, float* s) {
-  if (vec && kb + 4 <= n) {
-    const float4 v = *reinterpret_cast<const float4*>(row + kb);
-    s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (kb + i < n) s[i] = row[kb + i];
-  }
-}
 
 template <int BN, int CW>
 __global__ void __launch_bounds__(32 * (4 + CW), 1)
@@ -196,20 +183,12 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
       float acc[COLS];
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.f;
-      // scales are loaded a group of four blocks ahead: a row's lie together, so
-      // one 16-byte load (where the rows are aligned) serves four blocks, and no
-      // load is waited for where it is issued
-      float cur[4], nxt[4];
-      load_scales4(sa, 0, p.kb, p.sa_vec, nxt);
-      float sb_next = sb[0];
+      // scales are loaded a block ahead and multiplied where they are used, so that
+      // no load is waited for where it is issued
+      float sa_next = sa[0], sb_next = sb[0];
       for (int kb = 0; kb < p.kb && ok; ++kb, ++it) {
-        if ((kb & 3) == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
-          load_scales4(sa, kb + 4, p.kb, p.sa_vec, nxt);
-        }
-        const float s = (kb & 2 ? (kb & 1 ? cur[3] : cur[2]) : (kb & 1 ? cur[1] : cur[0])) * sb_next;
-        if (kb + 1 < p.kb) sb_next = sb[kb + 1];
+        const float s = sa_next * sb_next;
+        if (kb + 1 < p.kb) sa_next = sa[kb + 1], sb_next = sb[kb + 1];
         const uint32_t a = it % A, an = (it + 1) % A;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {

@@ -177,7 +177,6 @@ hs2_status hs2_fp8_gemm(const void* A, const float* A_scale, int64_t M, const vo
   p.N = N;
   p.K = K;
   p.kb = (K + kFgBK - 1) / kFgBK;
-  p.sa_vec = p.kb % 4 == 0 && aligned16(A_scale);
   cudaStream_t s = (cudaStream_t)stream;
   // Few rows: the whole machine streams B (8 rows x 1536 x 4096: 5.3 us against 12.0 with
   // the tiles of many rows; 64 rows: 12.3 us against 10.9, so not from there on).

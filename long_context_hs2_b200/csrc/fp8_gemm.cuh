@@ -66,6 +66,20 @@ struct FgSmem {
   static constexpr int kTmem = kAcc * BN;
 };
 
+// An accumulator that the CW consumer warps have read goes back to its MMA issuer
+// (one warp) by a named barrier: the mbarrier way back, an arrival and a wait
+// through shared memory that the MMAs' operands keep busy, was some 500 cycles of
+// the 1,200 that a 256-column accumulator waited between two uses (18,944 x 1536 x
+// 4096: 128 -> 115 us).
+template <int CW>
+__device__ __forceinline__ void fg_acc_arrive(int acc) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(1 + acc), "n"(32 * (CW + 1)) : "memory");
+}
+template <int CW>
+__device__ __forceinline__ void fg_acc_sync(int acc) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + acc), "n"(32 * (CW + 1)) : "memory");
+}
+
 template <int BN, int CW>
 __global__ void __launch_bounds__(32 * (4 + CW), 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap amap,
@@ -78,8 +92,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
   uint64_t* empty = full + SM::kStages;
   uint64_t* acc_full = empty + SM::kStages;    // [A]
-  uint64_t* acc_empty = acc_full + A;          // [A]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + A);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + A);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = p.m_tiles * p.n_tiles;
 
@@ -88,10 +101,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < A; ++a) {
-      mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], CW);
-    }
+    for (int a = 0; a < A; ++a) mbar_init(&acc_full[a], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -131,14 +141,14 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
       // next to a block's MMAs, pass while the other's MMAs run.
       const uint32_t total =
           (uint32_t)((tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x) * p.kb;
+      constexpr uint32_t idesc = tc_idesc_e4m3(128, BN);
       bool ok = true;
-      if (lane == 0) {
-        constexpr uint32_t idesc = tc_idesc_e4m3(128, BN);
-        for (uint32_t it = warp - 1; it < total; it += 2) {
-          const uint32_t s = it % SM::kStages, acc = it % A;
-          ok = mbar_wait(&full[s], (it / SM::kStages) & 1) &&
-               mbar_wait(&acc_empty[acc], ((it / A) & 1) ^ 1);
-          if (!ok) break;
+      for (uint32_t it = warp - 1; it < total; it += 2) {
+        const uint32_t s = it % SM::kStages, acc = it % A;
+        // (after a wait that gave up, reported, the barriers are still met)
+        if (ok) ok = mbar_wait(&full[s], (it / SM::kStages) & 1);
+        if (it >= (uint32_t)A) fg_acc_sync<CW>(acc);
+        if (ok && lane == 0) {
           tc_fence_after();
           const uint32_t addr = smem_u32(smem + s * SM::kStage);
           const uint64_t ad = sw128_kmajor_desc(addr), bd = sw128_kmajor_desc(addr + SM::kABytes);
@@ -148,11 +158,12 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
           tc_commit(&acc_full[acc]);
           tc_commit(&empty[s]);
         }
-        // the accumulators are read before tensor memory is given back
-        for (uint32_t i = total >= A ? total - A : 0; warp == 1 && i < total && ok; ++i)
-          ok = mbar_wait(&acc_empty[i % A], (i / A) & 1);
+        __syncwarp();
       }
-      __syncwarp();
+      // the accumulators are read before tensor memory is given back
+      for (uint32_t i = total >= A ? total - A : 0; i < total; ++i)
+        if ((i & 1) == (uint32_t)(warp - 1)) fg_acc_sync<CW>(i % A);
+      asm volatile("bar.sync 15, 64;" ::: "memory");
       if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, SM::kTmem);
@@ -173,9 +184,9 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
     float v[2][32];
     bool ok = mbar_wait(&acc_full[0], 0);
     tc_fence_after();
-    if (ok) tmem_ld32(taddr, v[0]);
+    tmem_ld32(taddr, v[0]);
     uint32_t it = 0;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       const int m = tile / p.n_tiles * 128 + quarter * 32 + lane;
       const int n0 = tile % p.n_tiles * BN + part * COLS;
       const float* sa = p.sa + (size_t)min(m, p.M - 1) * p.kb;
@@ -186,7 +197,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
       // scales are loaded a block ahead and multiplied where they are used, so that
       // no load is waited for where it is issued
       float sa_next = sa[0], sb_next = sb[0];
-      for (int kb = 0; kb < p.kb && ok; ++kb, ++it) {
+      for (int kb = 0; kb < p.kb; ++kb, ++it) {
         const float s = sa_next * sb_next;
         if (kb + 1 < p.kb) sa_next = sa[kb + 1], sb_next = sb[kb + 1];
         const uint32_t a = it % A, an = (it + 1) % A;
@@ -197,12 +208,13 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
             tmem_ld32(taddr + a * BN + (c + 1) * 32, v[(c + 1) & 1]);
           } else {
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[a]);
+            if (ok) fg_acc_arrive<CW>(a);
+            else fg_acc_sync<CW>(a);   // (in step with the issuer, which the wait was for)
             if (it + 1 < total) {
-              ok = mbar_wait(&acc_full[an], ((it + 1) / A) & 1);
+              // (after a wait that gave up, reported, the barriers are still met)
+              if (ok) ok = mbar_wait(&acc_full[an], ((it + 1) / A) & 1);
               tc_fence_after();
-              if (ok) tmem_ld32(taddr + an * BN, v[0]);
+              tmem_ld32(taddr + an * BN, v[0]);
             }
           }
 #pragma unroll

@@ -852,7 +852,8 @@ __global__ void __launch_bounds__(PwSmem<NR, FP8>::kThreads, 1)
   const bool any = work->x < work->y;
   PaWalk w;
   if (any) w.start(p.c, *work);
-  pdl_wait();
+  // Only the normalisers and the parts to join come from the attention kernel: the
+  // query and the joining warps wait for it, K and the queries are fetched before.
 
   if (any && warp == 0) {
     // ------------------------------------------------------------- producer
@@ -910,24 +911,26 @@ __global__ void __launch_bounds__(PwSmem<NR, FP8>::kThreads, 1)
     do {
       // both sets have ended the sequence before: its queries were used
       if (seg > 0 && !dead) dead = !mbar_wait(rs_free, (seg - 1) & 1);
+      for (int head = warp - 2; head < p.c.heads; head += 2)
+        pt_stage_q<NR, FP8>(p.q + ((size_t)w.b * p.H + (size_t)head * p.G) * 128, p.G,
+                            smem + SM::kQOff + head * SM::kQBytes, row_scale + head * NR);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      if (seg == 0) pdl_wait();
       for (int head = warp - 2; head < p.c.heads; head += 2) {
         const float lse = pa_item_lse(p, w.b, head, lane);
         if (lane < NR) neg_lse[head * NR + lane] = lane < p.G ? -lse : -INFINITY;
-        pt_stage_q<NR, FP8>(p.q + ((size_t)w.b * p.H + (size_t)head * p.G) * 128, p.G,
-                            smem + SM::kQOff + head * SM::kQBytes, row_scale + head * NR);
       }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(q_full);
-        mbar_arrive(rs_full);
-      }
+      if (lane == 0) mbar_arrive(rs_full);
       ++seg;
     } while (w.next(p.c, 1));
   } else if (warp >= 4 + 2 * kPtSet) {
     // ------------------------------------------- the cut items' outputs
     const int tid = threadIdx.x - 32 * (4 + 2 * kPtSet);
     PaJoin& join = *reinterpret_cast<PaJoin*>(smem + SM::kJoinOff);
+    pdl_wait();
     for (int row = blockIdx.x; row < p.c.B * p.H; row += gridDim.x)
       pa_join_row<128>(p, row, tid, join, false);
   } else if (any && warp >= 4) {

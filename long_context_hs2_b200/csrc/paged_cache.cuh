@@ -65,7 +65,7 @@ constexpr int kAppendRows = 64;     // rows of a CTA at most
 // lanes a row, the row's maximum taken by shuffles.  While the first loads are on
 // their way a thread per token finds its slot (bisecting row_start, then its page:
 // a chain of dependent loads, once per token).  Bound by HBM for prompts (65,536 tokens of
-// D = 128 to E4M3: APPENDUS us, APPENDGBS GB/s) and by one launch's latency for a
+// D = 128 to E4M3: 13.3 us, 3.8 TB/s) and by one launch's latency for a
 // decode step.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendParams p) {

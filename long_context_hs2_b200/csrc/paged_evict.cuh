@@ -11,8 +11,8 @@
 // keys it keeps in shared memory: no exchange, and the cluster only shares the
 // move.  More are split over the cluster: each CTA counts its part, sums its share
 // of the bins over all parts through distributed shared memory and hands the sums
-// to all, two barriers a digit.  (8 sequences of 32K: 28 us split, KSOLO32K us each for
-// itself; of 1216: 23 us and KSOLOFEW us: an exchange costs 4 us a digit.)  Counts
+// to all, two barriers a digit.  (8 sequences of 32K: 19 us split, 37 us each for
+// itself; of 1216: 23 us and 11 us.)  Counts
 // are whole numbers, so the result does not depend on the order of the atomics.
 // Survivors are then written in order from ballots: each warp owns a contiguous
 // run of candidates, counts it, learns what comes before it, and writes it.

@@ -77,6 +77,62 @@ def test_weights_accumulate(lens, H, heads, D, page, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,H,heads,page", [([150, 20, 300], 32, 32, 16), ([700, 129], 40, 20, 8),
+                                               ([260, 5], 160, 5, 64)])
+def test_weights_of_many_heads(lens, H, heads, page, fp8):
+    # more rows than the weights' tcgen05 pass keeps queries of (256), and an odd number of tiles
+    c = P.Cache(lens, page, heads, 128, fp8, seed=15, weight=True)
+    q = queries(c.B, H, 128, seed=16, size=2.0)
+    before = c.w.double()
+    o, lse = P.run_attention(c, q, 1 / math.sqrt(128), accumulate=True)
+    gain = check(c, q, o, lse, 1 / math.sqrt(128))
+    want = before + gain
+    assert ((c.weight.cpu().flatten().double() - want).abs() <= 1e-4 * gain + 2.0 ** -22 * want).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,page", [(128, 16), (64, 16), (128, 4)])
+def test_a_live_nan_stays_in_its_sequence(D, page, fp8):
+    lens = [300, 260, 140, 1, 90]
+    c = P.Cache(lens, page, 1, D, fp8, seed=17, weight=True)
+    for b, pool, j in ((0, c.kc, 37), (2, c.vc, 139)):
+        row = c.slots(b, [j])
+        (pool.view(torch.uint8) if fp8 else pool)[row] = 0x7f if fp8 else float("nan")
+    c.upload()
+    q = queries(c.B, 32, D, seed=18)
+    o, lse = P.run_attention(c, q, 1 / math.sqrt(D), accumulate=True)
+    assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.isnan(o[2]).all() and torch.isfinite(lse[2]).all()
+    eo, el, _, mass, floor = P.attention(c, q, 1 / math.sqrt(D))
+    for b in (1, 3, 4):
+        assert (lse[b].double() - el[b]).abs().max() <= 1e-4
+        tol = 2.0 ** -8 * eo[b].abs() + (2.0 ** -8 + 1e-4) * mass[b] + floor[b]
+        assert ((o[b].double() - eo[b]).abs() <= tol).all()
+    w = c.weight.cpu().flatten()
+    for b in (1, 3, 4):
+        assert torch.isfinite(w[c.slots(b, range(lens[b]))]).all()
+
+
+def test_call_after_call_and_side_by_side():
+    # two caches, two workspaces, two streams at once; then the same call twice in a row
+    cs = [P.Cache([3000, 17], 64, 1, 128, fp8, seed=19) for fp8 in (False, True)]
+    q = queries(2, 32, 128, seed=20)
+    want = [P.run_attention(c, q, 0.1) for c in cs]
+    n = hs2.hs2_paged_attn_workspace(2, 32, 1, 128)
+    qd = q.cuda()
+    bufs = [(torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(qd),
+             torch.empty(2, 32, device="cuda"), torch.cuda.Stream()) for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, (ws, o, lse, stream) in zip(cs, bufs):
+            hs2.hs2_paged_attn(qd, c.struct, 2, 32, 1, 128, 0.1, c.dt, o, lse, False, ws, n,
+                               stream=stream)
+    torch.cuda.synchronize()
+    for (ws, o, lse, _), (wo, wl) in zip(bufs, want):
+        assert torch.equal(o.cpu(), wo) and torch.equal(lse.cpu(), wl)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_long_ragged_batch(fp8):
     # more items than CTAs, and one sequence over many CTAs
     lens = [20000, 3, 0, 7000] + [(37 * i) % 300 for i in range(200)]

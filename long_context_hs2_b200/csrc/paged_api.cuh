@@ -49,6 +49,7 @@ PagedCache paged_params(const hs2_paged_cache* c, int B, int heads, hs2_kv_dtype
   p.page_shift = __builtin_ctz((unsigned)c->page_size);
   p.B = B;
   p.heads = heads;
+  p.scale_vec = heads == 1 && aligned16(p.k_scale) && aligned16(p.v_scale);
   return p;
 }
 

@@ -50,8 +50,12 @@ struct PtSmem {
   static constexpr int kPOff = kQOff + kQBytes;
   static constexpr int kPBytes = NR * 256;                       // P^T of a set
   static constexpr int kMetaOff = kPOff + 2 * kPBytes;
-  static constexpr int kMetaBytes = (FP8 ? 1024 : 0) + 64;
-  static constexpr int kRsOff = kMetaOff + kK * kMetaBytes;      // float [2][NR]: queries' scales
+  static constexpr int kMetaBytes = FP8 ? 1024 : 0;              // a K slot's scales
+  // masks of live positions, of 8 tiles: a tile's K is fetched after its softmax set
+  // gave back the K slot kK tiles before, and after the V of the tile before was
+  // fetched, so the tile kV before that one converted: every reader is within 8
+  static constexpr int kMaskOff = kMetaOff + kK * kMetaBytes;
+  static constexpr int kRsOff = kMaskOff + 8 * 16;               // float [2][NR]: queries' scales
   static constexpr int kRedOff = kRsOff + 2 * NR * 4;            // float [2 sets][4][NR]
   static constexpr int kRefOff = kRedOff + 8 * NR * 4;           // float [2 sets][NR]
   static constexpr int kBarOff = kRefOff + 2 * NR * 4;
@@ -141,39 +145,52 @@ struct PtRun {
   bool ok;
 };
 // The producer warp: tile t's K rows, scales and mask into a K slot.  id: the page
-// of the lane's run.  KONLY: the weights' pass, which wants every position's slot
-// and no v_scale.
+// of the lane's run.  KONLY: the weights' pass, which wants the runs' slots and no
+// v_scale.  A tile that is all positions takes the short way (the warp's time for a
+// tile bounds E4M3: position by position it was 1,300 cycles, and the 4 x 256K pass
+// 83 us): scales four at a time where they lie together, a mask of ones.
 template <bool FP8, bool KONLY>
 __device__ __forceinline__ PtRun pt_fetch_k(const PagedCache& c, const CUtensorMap* km,
-                                            uint8_t* kt, uint8_t* meta, uint64_t* full, int id,
-                                            int t, int len, int head, int* slots, uint64_t pol) {
+                                            uint8_t* kt, uint8_t* meta, unsigned* mask,
+                                            uint64_t* full, int id, int t, int len, int head,
+                                            int* slots, uint64_t pol) {
   const int lane = threadIdx.x & 31;
   const int shift = min(c.page_shift, 7), rows = 1 << shift;
   const int page_mask = (1 << c.page_shift) - 1, j0 = t * kPaTile;
-  unsigned live[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = i * 32 + lane;
-    const int page = __shfl_sync(0xffffffffu, id, key >> shift);
-    const bool ok = j0 + key < len && page >= 0;
-    live[i] = __ballot_sync(0xffffffffu, ok);
-    const int slot = (int)(((long long)page << c.page_shift) + ((j0 + key) & page_mask));
-    if (KONLY) slots[key] = slot;
-    if (FP8 && ok) {
-      const size_t at = (size_t)slot * c.heads + head;
-      cp_async4(smem_u32(meta) + key * 4, c.k_scale + at);
-      if (!KONLY) cp_async4(smem_u32(meta) + 512 + key * 4, c.v_scale + at);
+  const bool mine = lane < (kPaTile >> shift);
+  PtRun r;
+  r.ok = mine && j0 + lane * rows < len && id >= 0;
+  r.slot = (int)(((long long)id << c.page_shift) + ((j0 + lane * rows) & page_mask));
+  if (KONLY && mine) slots[lane] = r.slot;
+  const unsigned runs = __ballot_sync(0xffffffffu, r.ok);
+  const bool whole = j0 + kPaTile <= len && runs == __ballot_sync(0xffffffffu, mine);
+  if (whole) {
+    if (lane < 4) mask[lane] = 0xffffffffu;
+    if (FP8 && c.scale_vec) {
+      const int slot = __shfl_sync(0xffffffffu, r.slot, lane * 4 >> shift) + (lane * 4 & (rows - 1));
+      cp_async16(smem_u32(meta) + lane * 16, c.k_scale + slot, 16);
+      if (!KONLY) cp_async16(smem_u32(meta) + 512 + lane * 16, c.v_scale + slot, 16);
     }
   }
-  unsigned* mask = reinterpret_cast<unsigned*>(meta + (FP8 ? 1024 : 0));
-  if (lane < 4)
-    mask[lane] = lane == 0 ? live[0] : lane == 1 ? live[1] : lane == 2 ? live[2] : live[3];
+  if (!whole || (FP8 && !c.scale_vec)) {
+    unsigned live[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = i * 32 + lane, run = key >> shift;
+      const int slot = __shfl_sync(0xffffffffu, r.slot, run) + (key & (rows - 1));
+      const bool ok = j0 + key < len && (runs >> run & 1u);
+      live[i] = __ballot_sync(0xffffffffu, ok);
+      if (FP8 && ok) {
+        const size_t at = (size_t)slot * c.heads + head;
+        cp_async4(smem_u32(meta) + key * 4, c.k_scale + at);
+        if (!KONLY) cp_async4(smem_u32(meta) + 512 + key * 4, c.v_scale + at);
+      }
+    }
+    if (lane < 4)
+      mask[lane] = lane == 0 ? live[0] : lane == 1 ? live[1] : lane == 2 ? live[2] : live[3];
+  }
   __syncwarp();
-  PtRun r;
-  r.ok = lane < (kPaTile >> shift) && j0 + lane * rows < len && id >= 0;
-  r.slot = (int)(((long long)id << c.page_shift) + ((j0 + lane * rows) & page_mask));
-  const unsigned n = __popc(__ballot_sync(0xffffffffu, r.ok));
-  if (lane == 0) mbar_arrive_expect_tx(full, n * rows * (FP8 ? 128 : 256));
+  if (lane == 0) mbar_arrive_expect_tx(full, __popc(runs) * rows * (FP8 ? 128 : 256));
   __syncwarp();
   if (r.ok) {
     const uint32_t dst = smem_u32(kt) + lane * rows * 128;
@@ -345,6 +362,7 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kSlotOff);
   int4* work = reinterpret_cast<int4*>(smem + SM::kWorkOff);
   float* row_scale = reinterpret_cast<float*>(smem + SM::kRsOff);
+  unsigned* masks = reinterpret_cast<unsigned*>(smem + SM::kMaskOff);   // [8][4]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   pdl_launch_dependents();
@@ -355,8 +373,8 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < KN; ++i) {
       mbar_init(&kfull[i], pa_full_count(FP8, false));
-      // S^T is done with K, a softmax set (and the converters) with scales and mask
-      mbar_init(&kempty[i], 1 + kPtSet + (FP8 ? 4 : 0));
+      // S^T is done with K, and its softmax set has waited on the slot's arrival
+      mbar_init(&kempty[i], 1 + kPtSet);
     }
     for (int i = 0; i < VN; ++i) {
       mbar_init(&vfull[i], 1);
@@ -412,7 +430,7 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
           if (!ok) break;
           const PtRun r = pt_fetch_k<FP8, false>(
               p.c, &km, smem + ks * SM::kTile, smem + SM::kMetaOff + ks * SM::kMetaBytes,
-              &kfull[ks], pages.at(p.c, t), t, w.len, w.head, nullptr, kpol);
+              masks + (it & 7) * 4, &kfull[ks], pages.at(p.c, t), t, w.len, w.head, nullptr, kpol);
           if (it >= (uint32_t)VN) ok = mbar_wait(&vempty[vs], ((it / VN) - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -489,11 +507,10 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
     const uint32_t total = (uint32_t)(work->y - work->x);
     bool dead = false;
     for (uint32_t it = 0; any && it < total; ++it) {
-      const int ks = it % KN, vs = it % VN, hs = it % HN;
+      const int vs = it % VN, hs = it % HN;
       if (it >= (uint32_t)HN && !dead) dead = !mbar_wait(&h_empty[hs], ((it / HN) - 1) & 1);
       if (!dead) dead = !mbar_wait(&vfull[vs], (it / VN) & 1);   // after the mask was written
-      const unsigned word = reinterpret_cast<const unsigned*>(
-          smem + SM::kMetaOff + ks * SM::kMetaBytes + 1024)[row >> 5];
+      const unsigned word = masks[(it & 7) * 4 + (row >> 5)];
       const uint8_t* src = smem + SM::kVOff + vs * SM::kTile + row * 128;
       uint8_t* dst = smem + SM::kHOff + hs * 32768;
       // rows that are not positions become zeros, whatever they hold
@@ -516,7 +533,6 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&kempty[ks]);
         mbar_arrive(&vempty[vs]);
         mbar_arrive(&h_full[hs]);
       }
@@ -560,8 +576,7 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
         tmem_ldc<NC>(s_at, d);
         if (FP8) tmem_ldc<NC>(s_at + NR, d2);
         wait(&kfull[st], (it / KN) & 1);            // scales and mask
-        const unsigned word =
-            reinterpret_cast<const unsigned*>(meta + (FP8 ? 1024 : 0))[wq];
+        const unsigned word = masks[(it & 7) * 4 + wq];
         const bool live = word >> lane & 1u;
         float ks = 1.f, lv = 0.f, inv = 1.f;
         uint32_t flip = 0;
@@ -780,9 +795,9 @@ struct PwSmem {
   static constexpr int kQTerms = FP8 ? 2 : 1;
   static constexpr int kQOff = kK * kTile;
   static constexpr int kQBytes = NR * 256;                       // of one head
-  static constexpr int kMask = FP8 ? 1024 : 0, kSlots = kMask + 64;
+  static constexpr int kMask = FP8 ? 1024 : 0, kSlots = kMask + 16;
   static constexpr int kMetaOff = kQOff + kPwRows * 256;
-  static constexpr int kMetaBytes = kSlots + 512;
+  static constexpr int kMetaBytes = kSlots + 64;                 // scales, mask, runs' slots
   static constexpr int kRsOff = kMetaOff + kK * kMetaBytes;      // float [rows]: queries' scales
   static constexpr int kNlOff = kRsOff + kPwRows * 4;            // float [rows]: -lse (log2)
   static constexpr int kSumOff = kNlOff + kPwRows * 4;           // float [2 sets][2][128]
@@ -872,7 +887,8 @@ __global__ void __launch_bounds__(PwSmem<NR, FP8>::kThreads, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint8_t* meta = smem + SM::kMetaOff + ks * SM::kMetaBytes;
-          pt_fetch_k<FP8, true>(p.c, &km, smem + ks * SM::kTile, meta, &kfull[ks],
+          pt_fetch_k<FP8, true>(p.c, &km, smem + ks * SM::kTile, meta,
+                                reinterpret_cast<unsigned*>(meta + SM::kMask), &kfull[ks],
                                 u & 1 ? id1 : id0, t + (u & 1), w.len, u >> 1,
                                 reinterpret_cast<int*>(meta + SM::kSlots), kpol);
           ++it;
@@ -939,6 +955,7 @@ __global__ void __launch_bounds__(PwSmem<NR, FP8>::kThreads, 1)
     const int key = wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
     float* sums = reinterpret_cast<float*>(smem + SM::kSumOff) + set * 256;   // [2][128]
+    const int run_shift = min(p.c.page_shift, 7);   // of a page's rows in a tile
     uint32_t it0 = 0, seg = 0, turn = 0;            // it0: tiles met before the pair
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -966,7 +983,8 @@ __global__ void __launch_bounds__(PwSmem<NR, FP8>::kThreads, 1)
             wait(&kfull[st], (it / KN) & 1);
             const unsigned word = reinterpret_cast<const unsigned*>(meta + SM::kMask)[wq];
             live = word >> lane & 1u;
-            slot = reinterpret_cast<const int*>(meta + SM::kSlots)[key];
+            slot = reinterpret_cast<const int*>(meta + SM::kSlots)[key >> run_shift] +
+                   (key & ((1 << run_shift) - 1));
             const float ks = FP8 ? reinterpret_cast<const float*>(meta)[key] * p.scale_log2
                                  : p.scale_log2;
             tmem_ld_wait();

@@ -20,6 +20,7 @@ struct PagedCache {
   const int* page_table;   // [B][max_pages]
   const int* seq_len;      // [B]
   int n_pages, max_pages, page_shift, B, heads;
+  int scale_vec;           // one head, scales on 16 bytes: four positions' scales a load
 };
 
 // Length of sequence b's cache, held to what its page table can name (a longer

@@ -372,6 +372,11 @@ def hs2_paged_append(K, V, ld, n_rows, row_start, cache: hs2_paged_cache, B, kv_
     """K, V: the new rows, `ld` elements apart (views into a projection's output, for example)."""
     _check_cache("hs2_paged_append", cache, B, kv_heads, D, dt)
     n = n_rows * kv_heads * D
+    for rows in (K, V):
+        if not isinstance(rows, int) and rows is not None and (
+                rows.shape[0] < n_rows or rows.stride(-1) != 1
+                or (n_rows > 1 and rows.stride(0) != ld)):
+            raise Hs2Error("hs2_paged_append", 1)
     p = _tensors("hs2_paged_append", ((K, 2, n, False), (V, 2, n, False),
                                       (row_start, 4, B + 1, True)))
     _check("hs2_paged_append", load_library().hs2_paged_append(
@@ -400,7 +405,8 @@ def hs2_paged_evict(cache: hs2_paged_cache, B, kv_heads, D, dt, topk, window, ds
     """Keeps the `topk` heaviest positions and the `window` most recent ones of every sequence,
     moved to the pages of dst_table int32 [B, n] (None: in place)."""
     _check_cache("hs2_paged_evict", cache, B, kv_heads, D, dt)
-    p = _tensors("hs2_paged_evict", ((dst_table, 4, B, True), (kept, 4, B * (topk + window), True),
+    most = B if dst_table is None else B * dst_table.shape[1]
+    p = _tensors("hs2_paged_evict", ((dst_table, 4, most, True), (kept, 4, B * (topk + window), True),
                                      (new_len, 4, B, True)))
     _check("hs2_paged_evict", load_library().hs2_paged_evict(
         ctypes.byref(cache), B, kv_heads, D, dt, topk, window, p[0],

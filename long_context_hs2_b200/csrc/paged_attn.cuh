@@ -1,6 +1,10 @@
 // Attention of one new token per sequence over a paged cache, split over the
 // cache's length and joined; optionally every position's head-summed
-// probability is added to its accumulated weight.
+// probability is added to its accumulated weight.  This file: the shares of the
+// work, the join, and the kernels on warp MMAs, which serve head_dim 64 and pages
+// under 8 positions (777 positions, 8 heads x 64: 7.7 us with the join).  Larger
+// pages of head_dim 128: paged_attn_tc.cuh (4 x 256K E4M3: 122 us with these
+// kernels, bound by the warp MMAs and the codes' conversion, 76 there).
 //
 //   s_hj = scale <q_h, k_j>,  O_h = sum_j p_hj v_j,  p_hj = exp(s_hj - lse_h),
 //   lse_h = log sum_j exp(s_hj),  weight_j += sum_h p_hj        (j < seq_len)
@@ -73,7 +77,9 @@ struct PaShare {
   int total, chunk;
   __device__ __forceinline__ PaShare(int total_, int grid)
       : total(total_), chunk(max(1, (total_ + grid - 1) / grid)) {}
-  __device__ __forceinline__ int begin(int c) const { return (int)min((long long)total, (long long)c * chunk); }
+  __device__ __forceinline__ int begin(int c) const {
+    return (int)min((long long)total, (long long)c * chunk);
+  }
   __device__ __forceinline__ int owner(int g) const { return g / chunk; }
 };
 __device__ __forceinline__ int pa_tiles(int len) { return (len + kPaTile - 1) / kPaTile; }

@@ -142,6 +142,18 @@ def test_long_ragged_batch(fp8):
     check(c, q, o, lse, 1 / math.sqrt(128))
 
 
+@pytest.mark.parametrize("D,page,spare", [(64, 1, 0), (128, 1, 0), (128, 8, 0), (128, 512, 1)])
+def test_smallest_pools_and_empty_batches(D, page, spare):
+    for lens in ([1], [0, 0], [0, 1, 0]):
+        if sum(lens) + spare == 0:
+            spare = 1
+        c = P.Cache(lens, page, 1, D, False, seed=21, spare=spare, weight=True)
+        q = queries(c.B, 8, D, seed=22)
+        o, lse = P.run_attention(c, q, 0.1, accumulate=True)
+        gain = check(c, q, o, lse, 0.1)
+        assert ((c.weight.cpu().flatten().double() - c.w.double() - gain).abs() <= 2.0 ** -20).all()
+
+
 def test_sharp_softmax_raises_references_late():
     # logits that grow along the cache, the heaviest position last
     c = P.Cache([2000], 32, 1, 128, False, seed=8)

@@ -64,6 +64,16 @@ def test_norm_in_place_and_single_outputs():
     assert ((r.cpu().double() - h).abs() <= 2.0 ** -8 * h.abs()).all()
     want = h / torch.sqrt(h.square().mean(1, keepdim=True))
     assert ((y.cpu().double() - want).abs() <= (2.0 ** -8 + 2.0 ** -19) * want.abs()).all()
+    # the output in X's own buffer, the sum in X's
+    a, b = (torch.randn(5, 1040, generator=g).bfloat16().cuda() for _ in range(2))
+    w = torch.ones(1040, dtype=torch.bfloat16, device="cuda")
+    want_sum, want_y = torch.empty_like(a), torch.empty_like(a)
+    hs2.hs2_add_rmsnorm(a, b, w, 5, 1040, 1e-6, want_sum, want_y)
+    y2, s2 = a.clone(), a.clone()
+    hs2.hs2_add_rmsnorm(y2, b, w, 5, 1040, 1e-6, None, y2)
+    hs2.hs2_add_rmsnorm(s2, b, w, 5, 1040, 1e-6, s2)
+    status_ok()
+    assert torch.equal(y2, want_y) and torch.equal(s2, want_sum)
     # tiny values: the scale's reciprocal would overflow, the codes still stand for x
     gamma.fill_(2.0 ** -126)
     codes = torch.empty(9, 256, dtype=P.E4M3, device="cuda")
@@ -209,6 +219,35 @@ def test_evict_from_a_cache_beyond_shared_memory():
     # more candidates per CTA than it keeps in shared memory
     evict_case([250000, 10], 300, 16, 1, 64, 128, True, True, HEAVY)
     evict_case([250000], 5000, 16, 1, 64, 128, True, True, TIES)
+
+
+def test_evict_refuses_a_short_destination_table():
+    c = P.Cache([40, 40], 16, 1, 64, False, seed=31, weight=True)
+    kept = torch.empty(2, 24, dtype=torch.int32, device="cuda")
+    short = torch.zeros(1, 2, dtype=torch.int32, device="cuda")      # one row for two sequences
+    with pytest.raises(hs2.Hs2Error):
+        hs2.hs2_paged_evict(c.struct, 2, 1, 64, c.dt, 20, 4, short, kept, kept[:, 0].contiguous())
+
+
+def test_evict_twice_and_replayed():
+    # into the same pages twice, and from a graph: the source stays as it was
+    c = P.Cache([900, 300], 16, 2, 64, True, seed=32, weight=True, spare=2 * 8 + 1)
+    dst = c.free[:16].reshape(2, 8).cuda()
+    kept = torch.empty(2, 128, dtype=torch.int32, device="cuda")
+    new_len = torch.empty(2, dtype=torch.int32, device="cuda")
+    call = lambda: hs2.hs2_paged_evict(c.struct, 2, 2, 64, c.dt, 100, 28, dst, kept, new_len)  # noqa: E731
+    call()
+    status_ok()
+    first = [t.clone() for t in (c.k.view(torch.uint8), c.v_scale, c.weight, kept, new_len)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(2):
+        kept.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(first, (c.k.view(torch.uint8), c.v_scale, c.weight, kept, new_len)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
 def test_evict_large_batch():

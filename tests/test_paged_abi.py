@@ -119,3 +119,8 @@ def test_binding_checks_tensors(lib):
     with pytest.raises(hs2.Hs2Error):
         hs2.paged_cache(torch.zeros(2, 16, 1, 64), torch.zeros(2, 16, 1, 64),
                         torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    # rows that are not `ld` apart, or too few
+    rows = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for bad in (rows[:, ::2], rows[:3], rows):
+        with pytest.raises(hs2.Hs2Error):
+            hs2.hs2_paged_append(bad, bad, 128, 4, None, cache(), 4, 1, 64, 0, stream=0)

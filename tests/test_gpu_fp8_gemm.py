@@ -69,7 +69,8 @@ def test_sizes(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(5000, 1536, 256), (2500, 2049, 400), (20000, 40, 128),
-                                   (300, 8192, 128), (3, 5000, 2048), (128, 127, 16)])
+                                   (300, 8192, 128), (3, 5000, 2048), (128, 127, 16),
+                                   (20000, 333, 144), (9000, 1030, 64), (700, 36, 272)])
 def test_shapes_of_every_variant(M, N, K):
     check(*operands(M, N, K, seed=3))
 

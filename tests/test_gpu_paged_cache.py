@@ -24,7 +24,7 @@ def status_ok():
 
 # ----------------------------------------------------------------------- norm --
 @pytest.mark.parametrize("residual", [False, True])
-@pytest.mark.parametrize("T,hidden", [(1, 16), (5, 128), (33, 144), (7, 512), (6, 528), (3, 4096),
+@pytest.mark.parametrize("T,hidden", [(1, 16), (150, 16), (9, 48), (41, 80), (5, 128), (33, 144), (7, 512), (6, 528), (3, 4096),
                                       (2, 8208), (3, 16384), (2, 32768), (1000, 1040)])
 def test_norm(T, hidden, residual):
     g = torch.Generator().manual_seed(T + hidden)

@@ -318,3 +318,35 @@ def test_decode_steps_with_eviction(fp8):
             c.lens[b] = len(want)
         assert c.len_dev.tolist() == c.lens
     assert c.lens == [topk + window] * B
+
+
+def test_pools_beyond_32_bits():
+    """Pages whose rows lie more than 2^32 bytes into their pools give what the same pages
+    in a small pool give, bit for bit."""
+    page, D, lens = 64, 128, [200, 70]
+    small = P.Cache(lens, page, 1, D, False, seed=50, weight=True, stale=1.0, spare=4)
+    n = 300_000                                      # 4.9 GB for K and as much for V
+    high = n - small.n_pages                         # the small pool's pages, at the end
+    k, v = (torch.empty(n, page, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    weight = torch.empty(n, page, device="cuda")
+    for big, t in ((k, small.k), (v, small.v), (weight, small.weight)):
+        big[high:] = t
+    table = (small.table_dev.long().clamp(max=small.n_pages) + high).clamp(max=n - 1).int()
+    lens_dev = small.len_dev.clone()
+    big = hs2.paged_cache(k, v, table, lens_dev, weight=weight)
+    q = torch.randn(2, 32, D, generator=torch.Generator().manual_seed(51)).bfloat16().cuda()
+    rows = torch.randn(2, 2, D, generator=torch.Generator().manual_seed(52)).bfloat16().cuda()
+    ws = torch.empty(hs2.hs2_paged_attn_workspace(2, 32, 1, D), dtype=torch.uint8, device="cuda")
+    results = []
+    for cache, length in ((small.struct, small.len_dev), (big, lens_dev)):
+        o, lse = torch.empty_like(q), torch.empty(2, 32, device="cuda")
+        kept = torch.empty(2, 60, dtype=torch.int32, device="cuda")
+        hs2.hs2_paged_append(rows[:, 0], rows[:, 1], rows.stride(0), 2, None, cache, 2, 1, D, 0)
+        hs2.hs2_paged_attn(q, cache, 2, 32, 1, D, D ** -0.5, 0, o, lse, True, ws, ws.numel())
+        hs2.hs2_paged_evict(cache, 2, 1, D, 0, 40, 20, None, kept, length)
+        status_ok()
+        results.append((o, lse, kept, length))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    for t, s in ((k, small.k), (v, small.v), (weight, small.weight)):
+        assert torch.equal(t[high:], s)

@@ -483,6 +483,10 @@ HS2_API size_t hs2_paged_attn_workspace(int B, int H, int kv_heads, int D);
  *   s_hj = scale * <Q[b][h], K[j]>,  lse_h = log sum_j exp(s_hj)
  *   O[b][h] = sum_j exp(s_hj - lse_h) V[j]
  *   accumulate: weight_j += sum_h exp(s_hj - lse_h)  (all H heads)
+ * Logits, sums and O are fp32.  The probabilities go to the tensor cores as bf16
+ * (2^-8 of each term of O; lse and weights take them unrounded), over E4M3 pages
+ * their products with v_scale as two bf16 terms (2^-16 of each, at any scale); the
+ * sums want |V| < 1e30.
  * Q, O: bf16 [B][H][D]; lse: fp32 [B][H] or NULL.  seq_len[b] == 0: O = 0, lse =
  * -inf.  accumulate needs cache->weight, and pages that no two sequences share
  * (shared pages are fine without it).  H % kv_heads == 0, H / kv_heads <= 32, and

@@ -98,7 +98,7 @@ hs2_status run_paged_attn(const CUtensorMap& km, const CUtensorMap& vm, const Pa
   auto kw = paged_weight_kernel<MT, D, FP8>;
   hs2_status st;
   // tcgen05 for head_dim 128 where a page's rows are a TMA box of whole swizzle atoms (4 x
-  // 256K E4M3: 76 us against 122 with warp MMAs; 8 x up to 32K bf16: 18 against 30)
+  // 256K E4M3: 85 us against 122 with warp MMAs; 8 x up to 32K bf16: 18 against 30)
   if (D == 128 && p.c.page_shift >= 3) {
     using ST = PtSmem<16 * MT, FP8>;
     auto k = paged_attn_tc_kernel<16 * MT, FP8>;

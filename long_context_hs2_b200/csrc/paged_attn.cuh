@@ -4,7 +4,7 @@
 // work, the join, and the kernels on warp MMAs, which serve head_dim 64 and pages
 // under 8 positions (777 positions, 8 heads x 64: 7.7 us with the join).  Larger
 // pages of head_dim 128: paged_attn_tc.cuh (4 x 256K E4M3: 122 us with these
-// kernels, bound by the warp MMAs and the codes' conversion, 76 there).
+// kernels, bound by the warp MMAs and the codes' conversion, 85 there).
 //
 //   s_hj = scale <q_h, k_j>,  O_h = sum_j p_hj v_j,  p_hj = exp(s_hj - lse_h),
 //   lse_h = log sum_j exp(s_hj),  weight_j += sum_h p_hj        (j < seq_len)
@@ -32,12 +32,12 @@
 // replaced (never computed with), V rows are zeroed in shared memory, so what
 // stale pages hold -- infinities, NaN -- reaches no sum.
 //
-// E4M3: codes become f16 (exact) in registers.  The queries are scaled by a
-// power of two per row into f16's range, k_scale multiplies the logits, and
-// v_scale the probabilities relative to the largest v_scale met so far, so that
-// P stays in f16's range whatever the scales.  P is rounded to bf16 (bf16
-// cache) or f16 for the MMA: 2^-8 or 2^-11 of each term, below the bf16 output's
-// own rounding once summed.
+// E4M3: codes become f16 (K) or bf16 (V) in registers, exactly.  The queries are
+// scaled by a power of two per row into f16's range, k_scale multiplies the logits,
+// and v_scale the probabilities, whose product is split into two bf16 terms (2^-16
+// of it at any size: f16 has not the range for scales that differ, and a row of
+// zeros has the scale 1 whatever its neighbours have).  Over a bf16 cache P is one
+// bf16: 2^-8 of each term, as the bf16 output's own rounding.
 #pragma once
 
 #include "paged_cache.cuh"
@@ -56,7 +56,6 @@ constexpr bool kPaMove = MT == 2 && D == 128;
 template <int MT, int D>
 constexpr int kPaAttnThreads = kPaMove<MT, D> ? 32 * (kPaWarps + 4) : kPaThreads;
 constexpr float kPaSlack = 8.f;              // log2 a logit may exceed its reference by
-constexpr float kPaMinScale = 1e-30f;        // least reference of v_scale (its inverse is finite)
 constexpr float kPaLog2e = 1.4426950408889634f;
 constexpr float kPaLn2 = 0.6931471805599453f;
 
@@ -205,10 +204,18 @@ __device__ __forceinline__ void mma_f16_16816(float* d, uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// S += Q K^T: E4M3's codes as f16.
 template <bool FP8>
-__device__ __forceinline__ void pa_mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void pa_mma_qk(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   if (FP8) mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
   else mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+// O += P V, the terms of P one after the other.
+template <int TERMS>
+__device__ __forceinline__ void pa_mma_pv(float* d, const uint32_t (&a)[TERMS][4], uint32_t b0,
+                                          uint32_t b1) {
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) mma_bf16_16816(d, a[t][0], a[t][1], a[t][2], a[t][3], b0, b1);
 }
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(uint16_t)two, __NV_E4M3);
@@ -424,8 +431,8 @@ __device__ __forceinline__ void pa_scores(uint32_t qs, uint32_t kt, int key0,
       for (int m = 0; m < MT; ++m) {
         uint32_t a[4];
         ldsm_x4(qs + pa_q_at<MT, D>(m * 16 + qrow, 2 * (k0 + q) + qc), a[0], a[1], a[2], a[3]);
-        pa_mma<FP8>(s[m][0], a, lo[0], hi[0]);
-        pa_mma<FP8>(s[m][1], a, lo[1], hi[1]);
+        pa_mma_qk<FP8>(s[m][0], a, lo[0], hi[0]);
+        pa_mma_qk<FP8>(s[m][1], a, lo[1], hi[1]);
       }
     }
   }
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
     pa_load_q<MT, D, FP8>(p.q + ((size_t)w.b * p.H + (size_t)w.head * p.G) * D, p.G, qs,
                           row_scale);
     pa_consumers_sync();
-    float o[MT][D / 8][4], mref[MT][2], l[MT][2], f[MT][2], vref = 0.f, vinv = 0.f;
+    float o[MT][D / 8][4], mref[MT][2], l[MT][2], f[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -581,24 +588,7 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
                               fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1]));
             raise |= top[m][h] > mref[m][h] + kPaSlack;
           }
-        float vtop = 0.f;
-        if (FP8) {
-          vtop = fmaxf(fmaxf(fmaxf(fabsf(vs[0][0]), fabsf(vs[0][1])),
-                             fmaxf(fabsf(vs[1][0]), fabsf(vs[1][1]))), kPaMinScale);
-          raise |= vtop > vref;
-        }
         if (__any_sync(0xffffffffu, raise)) {
-          float vf = 1.f;
-          if (FP8) {
-#pragma unroll
-            for (int off = 2; off; off >>= 1)
-              vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
-            if (vtop > vref) {
-              vf = vref / vtop;
-              vref = vtop;
-              vinv = 1.f / vref;
-            }
-          }
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             float a[2];
@@ -617,15 +607,12 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[m][n][i] *= a[i >> 1] * vf;
+              for (int i = 0; i < 4; ++i) o[m][n][i] *= a[i >> 1];
           }
         }
         // P, in the MMA's A layout
-        uint32_t pa[MT][4];
-        if (FP8) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n) vs[n][0] *= vinv, vs[n][1] *= vinv;
-        }
+        constexpr int kTerms = FP8 ? 2 : 1;
+        uint32_t pa[MT][kTerms][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -636,12 +623,15 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
               e[i] = s[m][n][i] == -INFINITY ? 0.f : fast_exp2(s[m][n][i] - mref[m][i >> 1]);
               l[m][i >> 1] += e[i];
             }
-            if (FP8) {
-              pa[m][2 * n] = pack_f16(e[0] * vs[n][0], e[1] * vs[n][1]);
-              pa[m][2 * n + 1] = pack_f16(e[2] * vs[n][0], e[3] * vs[n][1]);
-            } else {
-              pa[m][2 * n] = pack_bf16(e[0], e[1]);
-              pa[m][2 * n + 1] = pack_bf16(e[2], e[3]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float x = FP8 ? e[2 * h] * vs[n][0] : e[2 * h];
+              const float y = FP8 ? e[2 * h + 1] * vs[n][1] : e[2 * h + 1];
+              pa[m][0][2 * n + h] = pack_bf16(x, y);
+              if (FP8) {
+                const float2 r = bf16x2_to_float2(pa[m][0][2 * n + h]);
+                pa[m][kTerms - 1][2 * n + h] = pack_bf16(x - r.x, y - r.y);
+              }
             }
           }
         const int vrow = key0 + ((lane >> 3) & 1) * 8 + (lane & 7), vc = lane >> 4;
@@ -655,12 +645,14 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
               // even columns of the 16, then odd ones
               const uint32_t ev = __byte_perm(r[2 * q], r[2 * q + 1], 0x6420);
               const uint32_t od = __byte_perm(r[2 * q], r[2 * q + 1], 0x7531);
-              const uint32_t e0 = e4m3x2_to_f16x2(ev & 0xffffu), e1 = e4m3x2_to_f16x2(ev >> 16);
-              const uint32_t o0 = e4m3x2_to_f16x2(od & 0xffffu), o1 = e4m3x2_to_f16x2(od >> 16);
+              const uint32_t e0 = e4m3x2_to_bf16x2((uint16_t)ev);
+              const uint32_t e1 = e4m3x2_to_bf16x2((uint16_t)(ev >> 16));
+              const uint32_t o0 = e4m3x2_to_bf16x2((uint16_t)od);
+              const uint32_t o1 = e4m3x2_to_bf16x2((uint16_t)(od >> 16));
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
-                pa_mma<true>(o[m][2 * (c + q)], pa[m], e0, e1);
-                pa_mma<true>(o[m][2 * (c + q) + 1], pa[m], o0, o1);
+                pa_mma_pv(o[m][2 * (c + q)], pa[m], e0, e1);
+                pa_mma_pv(o[m][2 * (c + q) + 1], pa[m], o0, o1);
               }
             }
           }
@@ -672,8 +664,8 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
                       r[3]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              pa_mma<false>(o[m][2 * c], pa[m], r[0], r[1]);
-              pa_mma<false>(o[m][2 * c + 1], pa[m], r[2], r[3]);
+              pa_mma_pv(o[m][2 * c], pa[m], r[0], r[1]);
+              pa_mma_pv(o[m][2 * c + 1], pa[m], r[2], r[3]);
             }
           }
         }
@@ -703,8 +695,7 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
 #pragma unroll
         for (int q = 0; q < kPaWarps; ++q)
           top = fmaxf(top, ml[q * (MT * 16) + m * 16 + h * 8 + g8].x);
-        f[m][h] = (mref[m][h] == -INFINITY ? 0.f : fast_exp2(mref[m][h] - top)) *
-                  (FP8 ? vref : 1.f);
+        f[m][h] = mref[m][h] == -INFINITY ? 0.f : fast_exp2(mref[m][h] - top);
       }
     float* buf = reinterpret_cast<float*>(smem + st * SM::kStage);   // [warp][row][kJoin]
     constexpr int C = SM::kJoin;

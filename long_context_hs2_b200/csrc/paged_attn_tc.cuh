@@ -2,9 +2,10 @@
 // head_dim 128 and pages of at least 8 positions.  Same definition, work shares
 // and workspace as paged_attn.cuh.
 //
-// Bound by HBM (K and V once) where a tile's chain keeps up: 8 x up to 32K bf16
+// Bound by HBM (K and V once) where a tile's work keeps up: 8 x up to 32K bf16
 // streams at the copy rate between a start and an end of 4 and 2 us; 4 x 256K E4M3
-// takes 1.1 us a tile and SM against 0.76 us of HBM time, 76 us in all.
+// takes 1.4 us a tile and SM against 0.76 us of HBM time, 85 us in all (76 without V's
+// conversion, 84 with one term of P, 81 without the vote on the references).
 //
 // Tiles are computed transposed, 128 positions each:
 //   S^T[128 positions][rows]  = K_tile . Q^T      (M = 128 positions)
@@ -15,17 +16,18 @@
 // thread, and the exponentials need no exchange.  Row references are registers,
 // the same in all threads of a row half; they are raised (O and the sums rescaled)
 // only when a logit passes one by 2^8, agreed on by a barrier with an OR.
-// A tile's chain (S^T, softmax, P, O^T) is latency, about 2,500 cycles, so two run
-// at once: even and odd tiles of a share belong to two sets of softmax warps with
-// references, sums and an O^T of their own, joined when an item ends.
+// A tile's chain (S^T, softmax, P, O^T) is latency, so two run at once: even and odd
+// tiles of a share belong to two sets of softmax warps with references, sums and an
+// O^T of their own, joined when an item ends.
 //
 // E4M3.  K's codes go to the tensor cores as they are (kind::f8f6f4); the queries
 // are split into two E4M3 terms instead, extra rows of the MMA's N: scaled by a
 // power of two per row to |q| < 256, q = q1 + q2 / 16, exact for bf16 values down
-// to 2^-13 of the row's largest, else off by 2^-14 of 128.  V becomes f16 (exact)
-// by four converter warps, P is f16.  v_scale is a factor of p, put into the
-// exponent: P = 2^(x + log2 v_scale - ref), and the row sum takes P / v_scale; so
-// P stays in f16's range whatever the scales are.
+// to 2^-13 of the row's largest, else off by 2^-14 of 128.  V becomes bf16 (exact)
+// by four converter warps.  P = p * v_scale is split into two bf16 terms as well,
+// 2^-16 of P at any size: scales have fp32's range, a position of little probability
+// may hold all there is of a column, and f16 would lose it beside a row of a larger
+// scale (a row of zeros has the scale 1).
 //
 // Warp roles: 0 TMA producer, 1 S^T and 3 O^T issuer, 2 queries, 4-11 and 12-19 the two
 // softmax sets (warp w: TMEM lanes 32 (w % 4) .., row half (w - 4) / 4 % 2), 20-23
@@ -37,22 +39,26 @@
 
 namespace hs2 {
 
-constexpr float kPtMinScale = 1e-30f;   // least |v_scale| in the exponent
 constexpr int kPtSet = 8;               // softmax warps of a set
 
 template <int NR, bool FP8>
 struct PtSmem {
   static constexpr int kThreads = 32 * (4 + 2 * kPtSet + (FP8 ? 4 : 0));
-  // rings: K tiles (with the tile's scales and mask), V tiles, E4M3's f16 V tiles
+  // rings: K tiles (with the tile's scales and mask), V tiles, E4M3's bf16 V tiles
   static constexpr int kTile = 128 * 128 * (FP8 ? 1 : 2);
-  static constexpr int kK = FP8 ? 4 : 3, kV = FP8 ? 4 : 3, kH = FP8 ? 2 : 0;
+  static constexpr int kK = FP8 ? 4 : 3, kV = 3, kH = FP8 ? 2 : 0;
   static constexpr int kQTerms = FP8 ? 2 : 1;
   static constexpr int kVOff = kK * kTile;
   static constexpr int kHOff = kVOff + kV * kTile;
   static constexpr int kQOff = kHOff + kH * 32768;
   static constexpr int kQBytes = NR * 256;                       // bf16, or two terms of codes
   static constexpr int kPOff = kQOff + kQBytes;
-  static constexpr int kPBytes = NR * 256;                       // P^T of a set
+  // P^T of a set.  bf16: NR rows of 128 positions (K-major).  E4M3: 128 positions of 64
+  // rows, one 128-byte swizzle row each (MN-major: a thread has all rows of its position
+  // and writes them as they are): the first terms' NR, then the second terms'; with NR =
+  // 16 the rest is not written, and its columns of O^T are not read.
+  static constexpr int kPRows = FP8 ? 64 : NR;
+  static constexpr int kPBytes = kPRows * 256;
   static constexpr int kMetaOff = kPOff + 2 * kPBytes;
   static constexpr int kMetaBytes = FP8 ? 1024 : 0;              // a K slot's scales
   // masks of live positions, of 8 tiles: a tile's K is fetched after its softmax set
@@ -69,7 +75,7 @@ struct PtSmem {
   static constexpr int kBytes = kWorkOff + 64 + 1024;
   // TMEM columns: S^T of four tiles, O^T of the two sets
   static constexpr int kSCols = kQTerms * NR, kOCol = 4 * kSCols;
-  static constexpr int kNeed = kOCol + 2 * NR;
+  static constexpr int kNeed = kOCol + 2 * kPRows;
   static constexpr int kTmem = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   // registers: of the launch's kRegs a thread, warps 0-3 and the converters give
   // some to the softmax warps
@@ -78,6 +84,7 @@ struct PtSmem {
   static_assert(128 * kFew + 512 * kMany + (FP8 ? 128 * kConv : 0) <= kThreads * kRegs,
                 "shares of the registers");
   static_assert(2 * kPBytes >= NR * 128 * 4, "a set's O^T fits the two P^T buffers");
+  static_assert(kNeed <= 512, "tensor memory");
 };
 
 // NC (8 or 16) consecutive columns.
@@ -325,15 +332,16 @@ __device__ __forceinline__ void pt_issue_qk(uint32_t d, uint32_t k, uint32_t q) 
     }
   }
 }
-// O^T (+)= V^T P^T.
-template <int NR, bool FP8>
+// O^T (+)= V^T P^T, PR rows; MN: P^T is MN-major.
+template <int PR, bool MN>
 __device__ __forceinline__ void pt_issue_pv(uint32_t d, uint32_t v, uint32_t pt, bool accumulate) {
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
     const uint32_t half = ks >> 2, off = (ks & 3) * 32;
     tc_mma_f16(d, sw128_mnmajor_desc(v + ks * 2048, 16384),
-               sw128_kmajor_desc(pt + half * (NR * 128) + off),
-               tc_idesc_f16(128, NR, FP8 ? kTcF16 : kTcBF16, true, false), accumulate || ks > 0);
+               MN ? sw128_mnmajor_desc(pt + ks * 2048, 16384)
+                  : sw128_kmajor_desc(pt + half * (PR * 128) + off),
+               tc_idesc_f16(128, PR, kTcBF16, true, MN), accumulate || ks > 0);
   }
 }
 
@@ -342,17 +350,18 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap km,
                          const __grid_constant__ CUtensorMap vm, const PagedAttnParams p) {
   using SM = PtSmem<NR, FP8>;
-  constexpr int NC = NR / 2, KN = SM::kK, VN = SM::kV, HN = FP8 ? SM::kH : 1;
+  constexpr int NC = NR / 2, PR = SM::kPRows, KN = SM::kK, VN = SM::kV, HN = FP8 ? SM::kH : 1;
   static_assert(SM::kBytes <= 232448, "shared memory per CTA");
   static_assert(SM::kWorkOff % 16 == 0 && SM::kBarOff % 8 == 0 && SM::kMetaOff % 16 == 0 &&
-                    SM::kMetaBytes % 16 == 0, "alignment of shared words");
+                    SM::kMetaBytes % 16 == 0 && SM::kPOff % 1024 == 0 && SM::kPBytes % 1024 == 0,
+                "alignment of shared words and operands");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
   uint64_t* kempty = kfull + KN;
   uint64_t* vfull = kempty + KN;
   uint64_t* vempty = vfull + VN;
-  uint64_t* h_full = vempty + VN;    // E4M3: a V tile is f16
+  uint64_t* h_full = vempty + VN;    // E4M3: a V tile is bf16
   uint64_t* h_empty = h_full + SM::kH;
   uint64_t* s_full = h_empty + SM::kH;   // [4]
   uint64_t* s_empty = s_full + 4;    // [4]
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
                  mbar_wait(&p_full[set], (it >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            pt_issue_pv<NR, FP8>(tmem + SM::kOCol + set * NR,
+            pt_issue_pv<PR, FP8>(tmem + SM::kOCol + set * PR,
                                  smem_u32(FP8 ? smem + SM::kHOff + hs * 32768
                                               : smem + SM::kVOff + vs * SM::kTile),
                                  p_addr + set * SM::kPBytes, t - w.t0 >= 2);
@@ -505,34 +514,45 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
       } while (w.next(p.c, p.c.heads));
     }
   } else if (FP8 && warp >= 4 + 2 * kPtSet) {
-    // ------------------------------------------------------- V to f16 tiles
+    // ------------------------------------------------------ V to bf16 tiles
     regs_give_up<SM::kConv>();
     const int row = threadIdx.x - 32 * (4 + 2 * kPtSet);
     const uint32_t total = (uint32_t)(work->y - work->x);
     bool dead = false;
     for (uint32_t it = 0; any && it < total; ++it) {
       const int vs = it % VN, hs = it % HN;
-      if (it >= (uint32_t)HN && !dead) dead = !mbar_wait(&h_empty[hs], ((it / HN) - 1) & 1);
       if (!dead) dead = !mbar_wait(&vfull[vs], (it / VN) & 1);   // after the mask was written
       const unsigned word = masks[(it & 7) * 4 + (row >> 5)];
-      const uint8_t* src = smem + SM::kVOff + vs * SM::kTile + row * 128;
-      uint8_t* dst = smem + SM::kHOff + hs * 32768;
-      // rows that are not positions become zeros, whatever they hold
-      const uint32_t keep = word >> lane & 1u ? 0xffffffffu : 0u;
+      const uint32_t r7 = (uint32_t)(row & 7) << 4;
+      const uint32_t from = smem_u32(smem + SM::kVOff + vs * SM::kTile) + row * 128 + r7;
+      const uint32_t to = smem_u32(smem + SM::kHOff + hs * 32768) + row * 128 + r7;
+      // half a row at a time: the first is read before the bf16 slot is waited for
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t cw[4][4];
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch) {
-        const uint4 c = *reinterpret_cast<const uint4*>(src + ((ch ^ (row & 7)) << 4));
-        const uint32_t cw[4] = {c.x & keep, c.y & keep, c.z & keep, c.w & keep};
-        uint32_t h[8];
+        for (int c = 0; c < 4; ++c) ld_shared_v4(from ^ (half * 64 + c * 16), cw[c]);
+        if (half == 0 && it >= (uint32_t)HN && !dead)
+          dead = !mbar_wait(&h_empty[hs], ((it / HN) - 1) & 1);
+        if (word != 0xffffffffu) {
+          // rows that are not positions become zeros, whatever they hold
+          const bool live = word >> lane & 1u;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          h[2 * q] = e4m3x2_to_f16x2(cw[q] & 0xffffu);
-          h[2 * q + 1] = e4m3x2_to_f16x2(cw[q] >> 16);
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) cw[c][q] = live ? cw[c][q] : 0u;
         }
-        *reinterpret_cast<uint4*>(dst + sw128_offset(row, ch * 32, 128)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(dst + sw128_offset(row, ch * 32 + 16, 128)) =
-            make_uint4(h[4], h[5], h[6], h[7]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t h[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            h[2 * q] = e4m3x2_to_bf16x2((uint16_t)cw[c][q]);
+            h[2 * q + 1] = e4m3x2_to_bf16x2((uint16_t)(cw[c][q] >> 16));
+          }
+          st_shared_v4((to ^ (c * 32)) + half * 16384, h[0], h[1], h[2], h[3]);
+          st_shared_v4((to ^ (c * 32 + 16)) + half * 16384, h[4], h[5], h[6], h[7]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -550,10 +570,12 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
     float* red = reinterpret_cast<float*>(smem + SM::kRedOff) + set * 4 * NR;
     float* ref = reinterpret_cast<float*>(smem + SM::kRefOff);        // [set][row]
-    // where this lane's two positions of rows c0 + (lane & 1), + 2, .. go in P^T
-    uint8_t* const p_row = smem + SM::kPOff + set * SM::kPBytes + (key >> 6) * (NR * 128) +
-                           (c0 + (lane & 1)) * 128 + (key & 6) * 2;
-    const int p_chunk = (key & 63) >> 3;
+    // where this lane's P goes in P^T.  bf16: two positions of rows c0 + (lane & 1), + 2, ..;
+    // E4M3: its position's rows
+    uint8_t* const p_row = smem + SM::kPOff + set * SM::kPBytes +
+                           (FP8 ? key * 128 : (key >> 6) * (NR * 128) + (c0 + (lane & 1)) * 128 +
+                                                  (key & 6) * 2);
+    const int p_chunk = FP8 ? key & 7 : (key & 63) >> 3;
     uint32_t it0 = 0, seg = 0;                      // the item's first tile, counted over the share
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -582,15 +604,10 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
         wait(&kfull[st], (it / KN) & 1);            // scales and mask
         const unsigned word = masks[(it & 7) * 4 + wq];
         const bool live = word >> lane & 1u;
-        float ks = 1.f, lv = 0.f, inv = 1.f;
-        uint32_t flip = 0;
+        float ks = 1.f, vscale = 1.f;
         if (FP8) {
           ks = reinterpret_cast<const float*>(meta)[key] * p.scale_log2;
-          const float vs = reinterpret_cast<const float*>(meta + 512)[key];
-          const float a = fmaxf(fabsf(vs), kPtMinScale);
-          flip = vs < 0.f ? 0x80008000u : 0u;
-          lv = __log2f(a);
-          inv = fast_rcp(a);
+          vscale = reinterpret_cast<const float*>(meta + 512)[key];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&kempty[st]);
@@ -598,7 +615,7 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
         if (FP8) {
 #pragma unroll
           for (int i = 0; i < NC; ++i)
-            d[i] = fmaf(fmaf(d2[i], 0.0625f, d[i]) * f[i], ks, lv - mref[i]);
+            d[i] = fmaf(fmaf(d2[i], 0.0625f, d[i]) * f[i], ks, -mref[i]);
         } else {
 #pragma unroll
           for (int i = 0; i < NC; ++i) d[i] = fmaf(d[i], p.scale_log2, -mref[i]);
@@ -607,7 +624,7 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[sb]);
         if (word != 0xffffffffu && !live) {         // replaced, not computed with
-          inv = 1.f;
+          vscale = 0.f;
 #pragma unroll
           for (int i = 0; i < NC; ++i) d[i] = -INFINITY;
         }
@@ -644,12 +661,15 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
           }
           if (!fresh) {
             tc_fence_after();
-            float o[NC];
-            tmem_ldc<NC>(lanes + SM::kOCol + set * NR + c0, o);
-            tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < NC; ++i) o[i] *= a[i];
-            tmem_stc<NC>(lanes + SM::kOCol + set * NR + c0, o);
+            for (int term = 0; term < (FP8 ? 2 * NR : NR); term += NR) {
+              float o[NC];
+              tmem_ldc<NC>(lanes + SM::kOCol + set * PR + term + c0, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < NC; ++i) o[i] *= a[i];
+              tmem_stc<NC>(lanes + SM::kOCol + set * PR + term + c0, o);
+            }
             tmem_st_wait();
             tc_fence_before();
           }
@@ -659,16 +679,37 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
           d[i] = fast_exp2(d[i]);
-          l[i] = fmaf(d[i], inv, l[i]);
+          l[i] += d[i];
+          if (FP8) d[i] *= vscale;
         }
+        if (FP8) {
+          // 8 rows at a time: the terms, and what the first term's rounding left
 #pragma unroll
-        for (int i = 0; i < NC; i += 2) {
-          // two rows of one position -> two positions of one row, over 2 lanes
-          const uint32_t v = FP8 ? pack_f16(d[i], d[i + 1]) ^ flip : pack_bf16(d[i], d[i + 1]);
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, v, 1);
-          *reinterpret_cast<uint32_t*>(p_row + i * 128 +
-                                       ((p_chunk ^ ((i + (lane & 1)) & 7)) << 4)) =
-              lane & 1 ? __byte_perm(other, v, 0x7632) : __byte_perm(v, other, 0x5410);
+          for (int i = 0; i < NC; i += 8) {
+            uint32_t v[4], r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float x = d[i + 2 * k], y = d[i + 2 * k + 1];
+              v[k] = pack_bf16(x, y);
+              const float2 back = bf16x2_to_float2(v[k]);
+              r[k] = pack_bf16(x - back.x, y - back.y);
+            }
+            const int ch = (c0 + i) >> 3;
+            *reinterpret_cast<uint4*>(p_row + ((ch ^ p_chunk) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(p_row + (((NR / 8 + ch) ^ p_chunk) << 4)) =
+                make_uint4(r[0], r[1], r[2], r[3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NC; i += 2) {
+            // two rows of one position -> two positions of one row, over 2 lanes
+            const uint32_t v = pack_bf16(d[i], d[i + 1]);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, v, 1);
+            *reinterpret_cast<uint32_t*>(p_row + i * 128 +
+                                         ((p_chunk ^ ((i + (lane & 1)) & 7)) << 4)) =
+                lane & 1 ? __byte_perm(other, v, 0x7632) : __byte_perm(v, other, 0x5410);
+          }
         }
         if (!FP8 && word != 0xffffffffu) {
           // rows that are not positions: zeros, whatever they held, before the product
@@ -714,8 +755,15 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
         const uint32_t last = it0 + skip + ((n - skip - 1) & ~1);
         wait(&pv_done[set], (last >> 1) & 1);
         tc_fence_after();
-        tmem_ldc<NC>(lanes + SM::kOCol + set * NR + c0, o);
+        tmem_ldc<NC>(lanes + SM::kOCol + set * PR + c0, o);
         tmem_ld_wait();
+        if (FP8) {
+          float o2[NC];
+          tmem_ldc<NC>(lanes + SM::kOCol + set * PR + NR + c0, o2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < NC; ++i) o[i] += o2[i];
+        }
         tc_fence_before();
       } else {
 #pragma unroll

@@ -1,0 +1,97 @@
+"""Values that the paged decode path meets at its edges, against the definitions in 64 bits:
+rows of zeros, scales of any size, infinities and NaN among live values.
+
+Tolerances.  As in test_gpu_paged_attn.py, without its floor: over E4M3 pages a probability
+times its v_scale goes to the tensor cores as two bf16 terms, which are off by 2^-8 * 2^-8 of
+it at any size, so |err| <= 2^-8 |o| + (2^-8 + 1e-4) * sum_j p_j |v_j|, and rows that add
+nothing to the output widen nothing.
+"""
+
+import math
+
+import pytest
+import torch
+
+import paged_testlib as P
+
+pytestmark = pytest.mark.gpu
+
+PATHS = [(128, 16), (64, 16), (128, 4)]      # head size, page: tcgen05, warp MMAs, small pages
+
+
+def pull(c, q, positions, gap):
+    """These positions of sequence 0 get a key whose logit (scale 1 / sqrt(D)) is `gap` nats for
+    every query row of q, which must share a direction: q[0, :, 0] == 8."""
+    rows = c.slots(0, positions)
+    c.kc.view(torch.uint8)[rows] = 0
+    c.kc.view(torch.uint8)[rows, :, 0] = 0x78                     # 256
+    c.ks[rows] = gap * math.sqrt(c.D) / (8 * 256.0)
+    c.k64[rows] = c.kc.view(torch.uint8)[rows].view(P.E4M3).double() * c.ks[rows].double()[..., None]
+
+
+def queries(B, H, D, seed=1):
+    q = 0.3 * torch.randn(B, H, D, generator=torch.Generator().manual_seed(seed))
+    q[:, :, 0] = 8
+    return q.bfloat16()
+
+
+def check(c, q, o, lse):
+    eo, el, gain, mass, _ = P.attention(c, q, c.D ** -0.5)
+    assert (lse.double() - el).abs().max() <= 1e-4
+    tol = 2.0 ** -8 * eo.abs() + (2.0 ** -8 + 1e-4) * mass
+    assert ((o.double() - eo).abs() <= tol).all(), ((o.double() - eo).abs() / tol).max()
+    return gain
+
+
+@pytest.mark.parametrize("D,page", PATHS)
+@pytest.mark.parametrize("gap,scale", [(10, 1e-3), (10, 1e-4), (10, 1e-7), (0, 1e-7), (20, 1e-5)])
+@pytest.mark.parametrize("codes", ["zeros", "one column"])
+def test_a_heavy_v_row_that_adds_little(D, page, gap, scale, codes):
+    # hs2_paged_append gives a row of zeros the scale 1, whatever its neighbours' scales are
+    c = P.Cache([700, 90], page, 1, D, True, seed=60, scale_range=(scale / 3, scale * 3), weight=True)
+    c.ks = c.ks * (1e-1 / scale)                          # logits of ordinary size
+    c.k64 = c.kc.double() * c.ks.double()[..., None]
+    c.k64[~c.live] = 0
+    q = queries(2, 32, D)
+    for j in (5, 300):
+        pull(c, q, [j], gap)
+        row = c.slots(0, [j])
+        c.vc.view(torch.uint8)[row] = 0
+        if codes == "one column":
+            c.vc.view(torch.uint8)[row, :, 3] = 0x7e         # 448
+        c.vs[row] = 1.0
+        c.v64[row] = c.vc.view(torch.uint8)[row].view(P.E4M3).double()
+    c.upload()
+    before = c.w.double()
+    o, lse = P.run_attention(c, q, D ** -0.5, accumulate=True)
+    gain = check(c, q, o, lse)
+    want = before + gain
+    assert ((c.weight.cpu().flatten().double() - want).abs() <= 1e-4 * gain + 2.0 ** -22 * want).all()
+
+
+@pytest.mark.parametrize("D,page", PATHS)
+@pytest.mark.parametrize("lo,hi", [(1e-35, 1e-33), (1e-30, 1e-3), (1e-12, 1e12), (1e20, 1e22)])
+def test_v_scales_of_any_size(D, page, lo, hi):
+    c = P.Cache([400, 33], page, 1, D, True, seed=61, scale_range=(lo, hi))
+    c.ks = torch.rand(c.ks.shape, generator=torch.Generator().manual_seed(2)) * 1e-2
+    c.k64 = c.kc.double() * c.ks.double()[..., None]
+    c.k64[~c.live] = 0
+    c.upload()
+    q = queries(2, 20, D, seed=62)
+    check(c, q, *P.run_attention(c, q, D ** -0.5))
+
+
+@pytest.mark.parametrize("D,page", PATHS)
+def test_a_flat_tail_under_peaks_without_values(D, page):
+    # every 50th position takes nearly all probability and has no value; the others' are 2^-27 of it
+    c = P.Cache([5000], page, 1, D, True, seed=63)
+    c.kc.view(torch.uint8)[c.live] = 0
+    c.k64 = torch.zeros_like(c.k64)
+    q = queries(1, 8, D, seed=64)
+    peaks = range(7, 5000, 50)
+    pull(c, q, peaks, 27 * math.log(2))
+    rows = c.slots(0, peaks)
+    c.vc.view(torch.uint8)[rows] = 0
+    c.v64[rows] = 0
+    c.upload()
+    check(c, q, *P.run_attention(c, q, D ** -0.5))

@@ -739,8 +739,10 @@ __global__ void __launch_bounds__(kPaAttnThreads<MT, D>, 1)
           }
 #pragma unroll
           for (int q = 0; q < kPaWarps; ++q) {
+            // a part without positions has the sum 0; one whose logits are all NaN has no
+            // reference either, and its sum is NaN
             const float2 v = ml[q * (MT * 16) + r];
-            if (v.x != -INFINITY) sum += v.y * fast_exp2(v.x - top);
+            if (v.y != 0.f) sum += v.y * fast_exp2(v.x == -INFINITY ? 0.f : v.x - top);
           }
           if (whole) {
             const size_t row = (size_t)w.b * p.H + (size_t)w.head * p.G + r;
@@ -805,8 +807,9 @@ __device__ __forceinline__ float pa_item_lse(const PagedAttnParams& p, int b, in
 #pragma unroll 8
   for (int c = parts.x; c <= parts.y; ++c) {
     const float2 v = p.part_ml[(size_t)(c * 2 + (c == parts.x)) * p.G + lane];
+    if (v.y == 0.f) continue;   // no positions
     const float m = fmaxf(top, v.x);
-    if (m != -INFINITY) sum = sum * fast_exp2(top - m) + v.y * fast_exp2(v.x - m);
+    sum = sum * fast_exp2(top - m) + v.y * fast_exp2(v.x - m);   // (NaN stays, m = -inf too)
     top = m;
   }
   return top + log2f(sum);

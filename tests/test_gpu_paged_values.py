@@ -95,3 +95,26 @@ def test_a_flat_tail_under_peaks_without_values(D, page):
     c.v64[rows] = 0
     c.upload()
     check(c, q, *P.run_attention(c, q, D ** -0.5))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,page", PATHS)
+def test_rows_of_nan(D, page, fp8):
+    # a NaN query; a sequence whose only key is NaN; sixteen NaN keys side by side
+    lens = [300, 1, 260, 700]
+    c = P.Cache(lens, page, 1, D, fp8, seed=67, weight=True)
+    for b, js in ((1, [0]), (2, range(128, 144)), (3, range(700))):
+        (c.kc.view(torch.uint8) if fp8 else c.kc)[c.slots(b, js)] = 0x7f if fp8 else float("nan")
+    c.upload()
+    q = torch.randn(4, 32, D, generator=torch.Generator().manual_seed(68)).bfloat16()
+    q[0, 9] = float("nan")
+    o, lse = P.run_attention(c, q, D ** -0.5, accumulate=True)
+    undefined = torch.zeros(4, 32, dtype=torch.bool)
+    undefined[1:] = True
+    undefined[0, 9] = True
+    assert torch.equal(torch.isnan(o).all(2), undefined)
+    assert torch.equal(torch.isnan(lse), undefined)
+    assert torch.isfinite(o[~undefined]).all() and torch.isfinite(lse[~undefined]).all()
+    w = c.weight.cpu().flatten()
+    for b, n in enumerate(lens):         # every head's probability is in the sum
+        assert torch.isnan(w[c.slots(b, range(n))]).all()

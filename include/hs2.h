@@ -483,6 +483,7 @@ HS2_API size_t hs2_paged_attn_workspace(int B, int H, int kv_heads, int D);
  *   s_hj = scale * <Q[b][h], K[j]>,  lse_h = log sum_j exp(s_hj)
  *   O[b][h] = sum_j exp(s_hj - lse_h) V[j]
  *   accumulate: weight_j += sum_h exp(s_hj - lse_h)  (all H heads)
+ * A query with an infinity has NaN for O over E4M3 pages, whatever the keys.
  * Logits, sums and O are fp32.  The probabilities go to the tensor cores as bf16
  * (2^-8 of each term of O; lse and weights take them unrounded), over E4M3 pages
  * their products with v_scale as two bf16 terms (2^-16 of each, at any scale); the

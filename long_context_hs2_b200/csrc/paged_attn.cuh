@@ -375,10 +375,12 @@ __device__ __forceinline__ void pa_load_q(const __nv_bfloat16* q, int G, uint8_t
 #pragma unroll
       for (int o = kLanes / 2; o; o >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      // 2^e <= amax < 2^(e+1); rows of zeros keep 1
+      // 2^e <= amax < 2^(e+1); rows of zeros keep 1.  A row with an infinity becomes NaN
+      // (its logits are infinite or NaN, its probabilities NaN)
       const int e = amax > 0.f ? max(-126, min(126, (int)(__float_as_uint(amax) >> 23) - 127)) : 0;
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      const float down = amax < INFINITY ? __uint_as_float((uint32_t)(127 - e) << 23)
+                                         : __uint_as_float(0x7fffffffu);
       if (ch == 0) row_scale[r] = up;
       // column c of 16 goes to place: c = 4 t + i, place = 2 t + (i & 1) + 8 (i >> 1)
 #pragma unroll

@@ -118,3 +118,24 @@ def test_rows_of_nan(D, page, fp8):
     w = c.weight.cpu().flatten()
     for b, n in enumerate(lens):         # every head's probability is in the sum
         assert torch.isnan(w[c.slots(b, range(n))]).all()
+
+
+@pytest.mark.parametrize("D,page", PATHS)
+@pytest.mark.parametrize("sign", [0, 1, -1])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_an_infinite_query_is_undefined(D, page, sign, value):
+    # its logits are infinities of one sign (all codes of that column of one sign) or of both,
+    # and exp(s - lse) is NaN in each case; no other row notices
+    c = P.Cache([300, 40], page, 1, D, True, seed=65)
+    if sign:
+        c.kc[:, :, 7] = (c.kc[:, :, 7].float().abs().clamp(min=1) * sign).to(P.E4M3)
+        c.k64 = c.kc.double() * c.ks.double()[..., None]
+        c.k64[~c.live] = 0
+        c.upload()
+    q = torch.randn(2, 32, D, generator=torch.Generator().manual_seed(66)).bfloat16()
+    q[0, 5, 7] = value
+    o, lse = P.run_attention(c, q, D ** -0.5)
+    assert torch.isnan(o[0, 5]).all() and not torch.isfinite(lse[0, 5])
+    q[0, 5] = 0
+    o[0, 5], lse[0, 5] = (t[0, 5] for t in P.run_attention(c, q, D ** -0.5))
+    check(c, q, o, lse)

@@ -56,19 +56,15 @@ PagedCache paged_params(const hs2_paged_cache* c, int B, int heads, hs2_kv_dtype
 // A K or V pool as [slots][heads][D], boxes of `rows` slots of one head.
 bool make_map_pool(CUtensorMap* map, const void* base, uint64_t slots, int heads, int D, int elem,
                    uint32_t rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   const cuuint64_t row = (cuuint64_t)D * elem;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, slots};
   cuuint64_t strides[2] = {row, row * heads};
   const uint32_t cols = (uint32_t)std::min(D, 128 / elem);
   cuuint32_t box[3] = {cols, 1, rows};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             cols * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(
+      map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base,
+      dims, strides, box,
+      cols * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // ----------------------------------------------------------- attention plan --

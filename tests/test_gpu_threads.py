@@ -1,6 +1,6 @@
-"""Host threads that make the same call with different sizes, each on its own stream and
-buffers: a kernel's settings belong to the function, and one thread's must not fail the
-other's launch."""
+"""Calls from several host threads, each on its own stream and buffers.  A kernel's settings
+belong to the function: one thread's must not fail another's launch.  A thread that has made
+no CUDA call yet has no context of its own: the first one may be this library's."""
 
 import threading
 
@@ -52,3 +52,45 @@ def test_evictions_of_caches_of_different_reach():
     side_by_side(calls)
     for kept, want, _ in results:
         assert kept[0].tolist() == want
+
+
+def test_the_first_cuda_call_of_a_thread():
+    g = torch.Generator().manual_seed(3)
+    a, b = (torch.randn(n, 256, generator=g).to(P.E4M3).cuda() for n in (64, 128))
+    sa, sb = torch.ones(64, 2, device="cuda"), torch.ones(1, 2, device="cuda")
+    c, few = (torch.zeros(m, 128, dtype=torch.bfloat16, device="cuda") for m in (64, 8))
+    w = P.Cache([300], 16, 1, 128, False, seed=4)
+    q = torch.randn(1, 8, 128, generator=g).bfloat16().cuda()
+    o, lse = torch.zeros_like(q), torch.zeros(1, 8, device="cuda")
+    n = hs2.hs2_paged_attn_workspace(1, 8, 1, 128)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    x, wt = (torch.randn(m, 256, generator=g).bfloat16().cuda() for m in (40, 256))
+    k, v = (torch.zeros(1, 40, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    stream = torch.cuda.current_stream().cuda_stream
+    calls = [lambda: hs2.hs2_fp8_gemm(a, sa, 64, b, sb, 128, 256, c, stream=stream),
+             lambda: hs2.hs2_fp8_gemm(a, sa, 8, b, sb, 128, 256, few, stream=stream),
+             lambda: hs2.hs2_paged_attn(q, w.struct, 1, 8, 1, 128, 0.1, 0, o, lse, False, ws, n,
+                                        stream=stream),
+             lambda: hs2.hs2_bridge_kv(x, 40, 256, wt, 1, 128, 0, [hs2.kv_cache(k, v)], 0,
+                                       stream=stream)]
+    outputs = [c, few, o, k]
+    for call, out in zip(calls, outputs):
+        call()
+        torch.cuda.synchronize()
+        want = out.clone()
+        out.zero_()
+        torch.cuda.synchronize()
+        errors = []
+
+        def run():
+            try:
+                call()
+            except Exception as e:      # noqa: BLE001 (told to the main thread)
+                errors.append(e)
+
+        t = threading.Thread(target=run)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not errors, errors
+        assert torch.equal(out, want)

@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(256) cp_rescale_kernel(float* o, const float* 
 }
 
 constexpr int kCpThreads = 256;
+constexpr int kCpMergeSmemMax = 200 * 1024;   // bytes of the G * topk keys of a row
 
 struct CpMergeParams {
   const float* cand_score;  // [G][rows][topk]; -1 where cand_idx is -1

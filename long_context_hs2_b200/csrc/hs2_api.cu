@@ -242,6 +242,9 @@ hs2_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, 
                    std::forward<Args>(args)...);
 }
 
+// Raises the kernel's limit of dynamic shared memory.  The limit belongs to the function:
+// give it the most that any call of the kernel takes, since another host thread may launch
+// between this one's setting it and its launch.
 template <typename K>
 bool set_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
@@ -263,7 +266,7 @@ hs2_status run_select(const FullAttnParams& fp, SelectParams sp, cudaStream_t s)
   const bool smem = seg <= kSelSmemMax;
   const int bytes = smem ? (int)std::max<long long>(16, seg * 4) : 0;
   auto k = smem ? select_topk_kernel<true> : select_topk_kernel<false>;
-  if (!set_smem(k, std::max(bytes, 16))) return HS2_ERR_CUDA;
+  if (!set_smem(k, smem ? kSelSmemMax * 4 : 16)) return HS2_ERR_CUDA;
   return launch(k, dim3((unsigned)(rows * cs)), dim3(kSelThreads), (size_t)bytes, s, cs, sp);
 }
 
@@ -375,7 +378,7 @@ hs2_status run_select_blocks(const FullAttnParams& fp, int topk, int window, int
   bp.qpos0 = fp.qpos0;
   const long long nblk_max = std::max<long long>(1, (fp.L - window) / block + 1);
   const size_t bytes = (size_t)(nblk_max + topk / block) * 4;
-  if (!set_smem(select_blocks_kernel, (int)bytes)) return HS2_ERR_CUDA;
+  if (!set_smem(select_blocks_kernel, (kBlkMaxBlocks + kBlkMaxKeep) * 4)) return HS2_ERR_CUDA;
   return launch(select_blocks_kernel, dim3((unsigned)((long long)fp.B * fp.T)), dim3(kBlkThreads),
                 bytes, s, 1, bp);
 }
@@ -759,7 +762,7 @@ hs2_status hs2_cp_merge_select(const float* cand_score, const int32_t* cand_idx,
   if (!cand_score || !cand_idx || !idx || !n_sel || G < 1 || B < 1 || T < 1 || topk < 1 ||
       window < 1 || topk + window > 4096 || q_pos0 < 0 || q_pos0 + T > INT32_MAX)
     return HS2_ERR_INVALID_ARG;
-  if ((int64_t)G * topk * 4 > 200 * 1024) return HS2_ERR_UNSUPPORTED;
+  if ((int64_t)G * topk * 4 > kCpMergeSmemMax) return HS2_ERR_UNSUPPORTED;
   CpMergeParams p;
   p.cand_score = cand_score;
   p.cand_idx = cand_idx;
@@ -772,7 +775,7 @@ hs2_status hs2_cp_merge_select(const float* cand_score, const int32_t* cand_idx,
   p.window = window;
   p.qpos0 = q_pos0;
   const int bytes = G * topk * 4;
-  if (!set_smem(cp_merge_select_kernel, bytes)) return HS2_ERR_CUDA;
+  if (!set_smem(cp_merge_select_kernel, kCpMergeSmemMax)) return HS2_ERR_CUDA;
   return launch(cp_merge_select_kernel, dim3((unsigned)p.rows), dim3(kCpThreads), (size_t)bytes,
                 (cudaStream_t)stream, 1, p);
 }

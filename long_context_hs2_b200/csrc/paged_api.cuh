@@ -356,9 +356,7 @@ hs2_status hs2_paged_evict(const hs2_paged_cache* cache, int B, int kv_heads, in
   int cs = kEvMaxCluster;
   while (cs > 1 && B * cs > sm_count() * 5 / 6) cs /= 2;
   p.cs = cs;
-  // shared memory for the keys that a CTA keeps; the function's limit is that of the
-  // largest caches, the same in every call: another host thread may launch between
-  // this one's setting it and its launch
+  // shared memory for the keys that a CTA keeps
   p.solo = (int)std::min<int64_t>(kEvSolo, std::max<int64_t>(1, reach - window));
   const size_t bytes = sizeof(EvSmem) + (size_t)p.solo * 4;
   auto k = fp8 ? paged_evict_kernel<true> : paged_evict_kernel<false>;

@@ -94,3 +94,52 @@ def test_the_first_cuda_call_of_a_thread():
         torch.cuda.synchronize()
         assert not errors, errors
         assert torch.equal(out, want)
+
+
+def test_merged_selections_of_different_sizes():
+    g = torch.Generator().manual_seed(2)
+    calls, results = [], []
+    for G, topk in ((12, 2000), (2, 16), (3, 40), (1, 8)):
+        score = torch.rand(G, 1, 1, topk, generator=g).cuda()
+        idx = torch.stack([torch.arange(r * topk, (r + 1) * topk) for r in range(G)]).int()
+        idx = idx.reshape(G, 1, 1, topk).cuda()
+        sel = torch.empty(1, 1, topk + 4, dtype=torch.int32, device="cuda")
+        n_sel = torch.empty(1, 1, dtype=torch.int32, device="cuda")
+        last = G * topk + 3                    # every candidate lies before the window
+        calls.append(lambda s, a=(score, idx, G, 1, 1, last, topk, 4, sel, n_sel):
+                     hs2.hs2_cp_merge_select(*a, stream=s))
+        best = torch.topk(score.flatten(), topk).indices.sort().values
+        results.append((sel, idx.flatten()[best].tolist() + list(range(last - 3, last + 1))))
+    side_by_side(calls)
+    for sel, want in results:
+        assert sel.flatten().tolist() == want
+
+
+def test_selections_of_different_lengths():
+    # token selection (after the separate passes of a chunk) and selection in blocks of one
+    H, D, topk, window = 32, 128, 8, 4
+    calls, results = [], []
+    for blocks in (False, True):
+        for L in (40000, 300, 400):
+            T = 1 if blocks else 4
+            k, v = (torch.randn(1, L, D, device="cuda").bfloat16() for _ in range(2))
+            q = torch.randn(1, T, H, D, device="cuda").bfloat16()
+            kv = hs2.kv_cache(k, v)
+            n = hs2.hs2_full_attn_select_workspace(1, T, L, H, D, topk, window, 0)
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+            o, lse = torch.empty(1, T, H, D, device="cuda"), torch.empty(1, T, H, device="cuda")
+            idx = torch.empty(1, T, topk + window, dtype=torch.int32, device="cuda")
+            ns = torch.empty(1, T, dtype=torch.int32, device="cuda")
+            head = (q, kv, 1, T, L, H, D, D ** -0.5, topk, window)
+            tail = (0, o, lse, idx, ns, ws, n)
+            call = ((lambda s, a=head + (1,) + tail: hs2.hs2_full_attn_select_blocks(*a, stream=s))
+                    if blocks else
+                    (lambda s, a=head + tail: hs2.hs2_full_attn_select(*a, stream=s)))
+            call(None)
+            torch.cuda.synchronize()
+            calls.append(call)
+            results.append((idx, idx.clone(), ws, k, v))
+    side_by_side(calls[:3], 4000)
+    side_by_side(calls[3:], 4000)
+    for idx, want, *_ in results:
+        assert torch.equal(idx, want)

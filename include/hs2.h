@@ -458,7 +458,7 @@ HS2_API hs2_status hs2_fp8_gemm(const void* A, const float* A_scale, int64_t M, 
  * hs2_paged_append -- the new tokens' K and V rows to their pages.
  * Sequence b's new tokens are rows row_start[b] .. row_start[b+1]-1 (int32
  * [B + 1], device, ascending; rows outside row_start[0] .. row_start[B]-1 are
- * not read), and they are its last positions: seq_len already counts them.
+ * not read, so n_rows may be an upper bound), and they are its last positions: seq_len already counts them.
  * row_start NULL: one new token per sequence, row b, n_rows == B.
  *   K, V: bf16, row r's [kv_heads][D] at r * ld elements (ld >= kv_heads * D,
  *         ld % 8 == 0: K and V may lie side by side in a projection's output).

@@ -1,5 +1,6 @@
 """Values that the paged decode path meets at its edges, against the definitions in 64 bits:
-rows of zeros, scales of any size, infinities and NaN among live values.
+rows of zeros, scales of any size, infinities and NaN among live values, rows that are no
+token's.
 
 Tolerances.  As in test_gpu_paged_attn.py, without its floor: over E4M3 pages a probability
 times its v_scale goes to the tensor cores as two bf16 terms, which are off by 2^-8 * 2^-8 of
@@ -12,6 +13,7 @@ import math
 import pytest
 import torch
 
+import long_context_hs2_b200 as hs2
 import paged_testlib as P
 
 pytestmark = pytest.mark.gpu
@@ -139,3 +141,34 @@ def test_an_infinite_query_is_undefined(D, page, sign, value):
     q[0, 5] = 0
     o[0, 5], lse[0, 5] = (t[0, 5] for t in P.run_attention(c, q, D ** -0.5))
     check(c, q, o, lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lead,n_rows", [(0, 50_000), (37, 5_000), (64, 107)])
+def test_append_with_an_upper_bound_of_rows(lead, n_rows, fp8):
+    # K and V hold the 43 tokens' rows only; row `lead` of the call is their first
+    lens, rows = [40, 3, 9], [31, 3, 9]
+    c = P.Cache(lens, 16, 2, 64, fp8, seed=70, weight=True)
+    kv = torch.randn(2, sum(rows), 128, generator=torch.Generator().manual_seed(71)).bfloat16()
+    dev = kv.cuda()
+    start = torch.tensor([lead, lead + 31, lead + 34, lead + 43], dtype=torch.int32, device="cuda")
+    k, v = (t.data_ptr() - lead * 128 * 2 for t in dev)
+    before = c.pools()
+    hs2.hs2_paged_append(k, v, 128, n_rows, start, c.struct, 3, 2, 64, c.dt)
+    assert hs2.hs2_last_device_status() == 0
+    after = c.pools()
+    touched = torch.zeros(c.n_pages * 16, dtype=torch.bool)
+    for b, n in enumerate(rows):
+        slots = c.slots(b, range(lens[b] - n, lens[b]))
+        touched[slots] = True
+        for name, x in zip(("k", "v"), kv[:, sum(rows[:b]):sum(rows[:b + 1])].unflatten(-1, (2, 64))):
+            if fp8:
+                got = after[name + "_scale"][slots]
+                assert ((got.double() - x.double().abs().amax(-1) / 448).abs()
+                        <= 2.0 ** -23 * got).all()
+                P.assert_codes(after[name][slots], x, got[..., None], 2.0 ** -22 * x.double().abs())
+            else:
+                assert torch.equal(after[name][slots], x)
+    for name, t in after.items():
+        bits = lambda a: a[~touched].contiguous().view(torch.uint8)     # noqa: E731
+        assert torch.equal(bits(t), bits(before[name])), name

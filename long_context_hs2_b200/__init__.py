@@ -298,19 +298,34 @@ def hs2_cp_merge_select(cand_score, cand_idx, G, B, T, q_pos0, topk, window, idx
 # Tensors given to these calls must be contiguous (K and V of the append excepted),
 # of the type the C ABI names, and on the current device, whose current stream the
 # work is enqueued on; anything else raises Hs2Error (invalid argument).  E4M3
-# codes are uint8 or float8_e4m3fn tensors.  Raw pointers are taken as they are.
+# codes are uint8 or float8_e4m3fn tensors, workspaces of any type of one byte.  Raw
+# pointers are taken as they are.
+_TYPES = {}
+
+
+def _types():
+    """The element types that each kind of argument may have."""
+    if not _TYPES:
+        import torch
+        codes = (torch.uint8, torch.float8_e4m3fn)
+        _TYPES.update(bf16=(torch.bfloat16,), f32=(torch.float32,), i32=(torch.int32,), e4m3=codes,
+                      bytes=codes + (torch.int8,))
+    return _TYPES
+
+
 def _tensors(fn: str, specs):
-    """Device pointers of (tensor, element size, least elements, contiguous) entries."""
+    """Device pointers of (tensor, kind of element, least elements, contiguous) entries."""
     import torch
+    types = _types()
     dev, out = None, []
-    for t, size, least, contiguous in specs:
+    for t, kind, least, contiguous in specs:
         if t is None or isinstance(t, int):
             out.append(t)
             continue
         d = t.get_device()
         if dev is None and d >= 0:
             dev = torch.cuda.current_device()
-        if (d != dev or t.element_size() != size or t.numel() < least
+        if (d != dev or t.dtype not in types[kind] or t.numel() < least
                 or (contiguous and not t.is_contiguous())):
             raise Hs2Error(fn, 1)
         out.append(t.data_ptr())
@@ -325,14 +340,13 @@ def paged_cache(k, v, page_table, seq_len, k_scale=None, v_scale=None,
     n_pages, page_size, heads, _ = k.shape
     if (v.shape != k.shape or v.dtype != k.dtype or page_table.dim() != 2
             or seq_len.numel() != page_table.shape[0]
-            or (k_scale is None) != (v_scale is None) or (k_scale is None) != (k.element_size() == 2)):
+            or (k_scale is None) != (v_scale is None)):
         raise Hs2Error("paged_cache", 1)
-    rows = n_pages * page_size
-    p = _tensors("paged_cache", ((k, 2 if k_scale is None else 1, 1, True),
-                                 (v, 2 if k_scale is None else 1, 1, True),
-                                 (k_scale, 4, rows * heads, True), (v_scale, 4, rows * heads, True),
-                                 (weight, 4, rows, True), (page_table, 4, 1, True),
-                                 (seq_len, 4, 1, True)))
+    rows, kind = n_pages * page_size, "bf16" if k_scale is None else "e4m3"
+    p = _tensors("paged_cache", ((k, kind, 1, True), (v, kind, 1, True),
+                                 (k_scale, "f32", rows * heads, True),
+                                 (v_scale, "f32", rows * heads, True), (weight, "f32", rows, True),
+                                 (page_table, "i32", 1, True), (seq_len, "i32", 1, True)))
     c = hs2_paged_cache(hs2_kv_cache(p[0], p[1], p[2], p[3]), p[4], p[5], p[6], n_pages, page_size,
                         page_table.shape[1])
     c._tensors = (k, v, page_table, seq_len, k_scale, v_scale, weight)
@@ -350,9 +364,10 @@ def _check_cache(fn: str, cache, B, kv_heads, D, dt):
 def hs2_add_rmsnorm(X, R, gamma, T, hidden, eps, sum=None, Y=None, Yq=None, Yq_scale=None,
                     stream=None):
     n = T * hidden
-    p = _tensors("hs2_add_rmsnorm", ((X, 2, n, True), (R, 2, n, True), (gamma, 2, hidden, True),
-                                     (sum, 2, n, True), (Y, 2, n, True), (Yq, 1, n, True),
-                                     (Yq_scale, 4, T * ((hidden + 127) // 128), True)))
+    p = _tensors("hs2_add_rmsnorm", ((X, "bf16", n, True), (R, "bf16", n, True),
+                                     (gamma, "bf16", hidden, True), (sum, "bf16", n, True),
+                                     (Y, "bf16", n, True), (Yq, "e4m3", n, True),
+                                     (Yq_scale, "f32", T * ((hidden + 127) // 128), True)))
     _check("hs2_add_rmsnorm", load_library().hs2_add_rmsnorm(
         p[0], p[1], p[2], T, hidden, eps, p[3], p[4], p[5], p[6], _stream(stream)))
 
@@ -360,9 +375,10 @@ def hs2_add_rmsnorm(X, R, gamma, T, hidden, eps, sum=None, Y=None, Yq=None, Yq_s
 def hs2_fp8_gemm(A, A_scale, M, B, B_scale, N, K, C, stream=None):
     """C = A B^T in E4M3 with a scale per 1 x 128 of A and 128 x 128 of B; C bf16 [M, N]."""
     kb = (K + 127) // 128
-    p = _tensors("hs2_fp8_gemm", ((A, 1, M * K, True), (A_scale, 4, M * kb, True),
-                                  (B, 1, N * K, True),
-                                  (B_scale, 4, (N + 127) // 128 * kb, True), (C, 2, M * N, True)))
+    p = _tensors("hs2_fp8_gemm", ((A, "e4m3", M * K, True), (A_scale, "f32", M * kb, True),
+                                  (B, "e4m3", N * K, True),
+                                  (B_scale, "f32", (N + 127) // 128 * kb, True),
+                                  (C, "bf16", M * N, True)))
     _check("hs2_fp8_gemm", load_library().hs2_fp8_gemm(p[0], p[1], M, p[2], p[3], N, K, p[4],
                                                        _stream(stream)))
 
@@ -377,8 +393,8 @@ def hs2_paged_append(K, V, ld, n_rows, row_start, cache: hs2_paged_cache, B, kv_
                 rows.shape[0] < n_rows or rows.stride(-1) != 1
                 or (n_rows > 1 and rows.stride(0) != ld)):
             raise Hs2Error("hs2_paged_append", 1)
-    p = _tensors("hs2_paged_append", ((K, 2, n, False), (V, 2, n, False),
-                                      (row_start, 4, B + 1, True)))
+    p = _tensors("hs2_paged_append", ((K, "bf16", n, False), (V, "bf16", n, False),
+                                      (row_start, "i32", B + 1, True)))
     _check("hs2_paged_append", load_library().hs2_paged_append(
         p[0], p[1], ld, n_rows, p[2], ctypes.byref(cache), B, kv_heads, D, dt, _stream(stream)))
 
@@ -393,8 +409,9 @@ def hs2_paged_attn(Q, cache: hs2_paged_cache, B, H, kv_heads, D, scale, dt, O, l
     head-summed probability to the cache's weight."""
     _check_cache("hs2_paged_attn", cache, B, kv_heads, D, dt)
     n = B * H * D
-    p = _tensors("hs2_paged_attn", ((Q, 2, n, True), (O, 2, n, True), (lse, 4, B * H, True),
-                                    (workspace, 1, workspace_bytes, True)))
+    p = _tensors("hs2_paged_attn", ((Q, "bf16", n, True), (O, "bf16", n, True),
+                                    (lse, "f32", B * H, True),
+                                    (workspace, "bytes", workspace_bytes, True)))
     _check("hs2_paged_attn", load_library().hs2_paged_attn(
         p[0], ctypes.byref(cache), B, H, kv_heads, D, scale, dt, p[1], p[2],
         1 if accumulate else 0, p[3], workspace_bytes, _stream(stream)))
@@ -406,8 +423,9 @@ def hs2_paged_evict(cache: hs2_paged_cache, B, kv_heads, D, dt, topk, window, ds
     moved to the pages of dst_table int32 [B, n] (None: in place)."""
     _check_cache("hs2_paged_evict", cache, B, kv_heads, D, dt)
     most = B if dst_table is None else B * dst_table.shape[1]
-    p = _tensors("hs2_paged_evict", ((dst_table, 4, most, True), (kept, 4, B * (topk + window), True),
-                                     (new_len, 4, B, True)))
+    p = _tensors("hs2_paged_evict", ((dst_table, "i32", most, True),
+                                     (kept, "i32", B * (topk + window), True),
+                                     (new_len, "i32", B, True)))
     _check("hs2_paged_evict", load_library().hs2_paged_evict(
         ctypes.byref(cache), B, kv_heads, D, dt, topk, window, p[0],
         0 if dst_table is None else dst_table.shape[1], p[1], p[2], _stream(stream)))

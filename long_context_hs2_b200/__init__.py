@@ -383,6 +383,17 @@ def hs2_fp8_gemm(A, A_scale, M, B, B_scale, N, K, C, stream=None):
                                                        _stream(stream)))
 
 
+def _row_elements(rows) -> int:
+    """Elements that lie one after another from the start of each row rows[r]; 0 where a row
+    has gaps."""
+    n = 1
+    for size, stride in zip(reversed(rows.shape[1:]), reversed(rows.stride()[1:])):
+        if size != 1 and stride != n:
+            return 0
+        n *= size
+    return n if rows.dim() > 1 else 0
+
+
 def hs2_paged_append(K, V, ld, n_rows, row_start, cache: hs2_paged_cache, B, kv_heads, D, dt,
                      stream=None):
     """K, V: the new rows, `ld` elements apart (views into a projection's output, for example)."""
@@ -390,8 +401,8 @@ def hs2_paged_append(K, V, ld, n_rows, row_start, cache: hs2_paged_cache, B, kv_
     n = n_rows * kv_heads * D
     for rows in (K, V):
         if not isinstance(rows, int) and rows is not None and (
-                rows.shape[0] < n_rows or rows.stride(-1) != 1
-                or (n_rows > 1 and rows.stride(0) != ld)):
+                rows.shape[0] < n_rows or (n_rows > 1 and rows.stride(0) != ld)
+                or _row_elements(rows) < kv_heads * D):
             raise Hs2Error("hs2_paged_append", 1)
     p = _tensors("hs2_paged_append", ((K, "bf16", n, False), (V, "bf16", n, False),
                                       (row_start, "i32", B + 1, True)))

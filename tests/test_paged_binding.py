@@ -128,3 +128,23 @@ def test_workspaces_are_bytes(calls):
     for dtype in (F32, torch.float16):
         with pytest.raises(hs2.Hs2Error):
             attn(workspace=t((1000,), dtype))
+
+
+def test_append_takes_rows_without_gaps(calls):
+    kv = t((7, 2, 2, 64), BF16)                    # K and V side by side, heads apart
+    append(K=kv[:, 0], V=kv[:, 1], ld=256)
+    append(K=kv.flatten(1)[:, :128], V=kv.flatten(1)[:, 128:], ld=256)
+    append(K=t((7, 1, 2, 64), BF16), V=t((9, 2, 64), BF16))
+    append(K=t((7, 2, 64), BF16)[:1], V=t((1, 128), BF16), n_rows=1, ld=4096)   # one row: no distance
+    assert len(calls) == 4
+    for bad, ld in ((t((7, 2, 2, 64), BF16)[:, :, 0], 256),       # heads 2 D apart
+                    (t((7, 64, 2), BF16).transpose(1, 2), 128),   # [heads][D] not in order
+                    (t((7, 2, 128), BF16)[:, :, :64], 256),       # a gap behind every head
+                    (t((7, 128, 2), BF16)[:, :, 0], 256),         # every other element
+                    (t((14, 64), BF16), 64),                      # half rows
+                    (t((14, 192), BF16)[:, :64], 192),            # half rows of a wider tensor
+                    (t((896,), BF16), 1)):
+        for kw in (dict(K=bad), dict(V=bad)):
+            with pytest.raises(hs2.Hs2Error):
+                append(ld=ld, **dict(dict(K=t((7, ld), BF16), V=t((7, ld), BF16)), **kw))
+    assert len(calls) == 4

@@ -429,14 +429,23 @@ def hs2_paged_attn(Q, cache: hs2_paged_cache, B, H, kv_heads, D, scale, dt, O, l
 
 
 def hs2_paged_evict(cache: hs2_paged_cache, B, kv_heads, D, dt, topk, window, dst_table, kept,
-                    new_len, stream=None):
+                    new_len, stream=None, dst_max_pages=None):
     """Keeps the `topk` heaviest positions and the `window` most recent ones of every sequence,
-    moved to the pages of dst_table int32 [B, n] (None: in place)."""
+    moved to the pages of dst_table int32 [B, dst_max_pages] (None: in place).  The width is
+    the tensor's own; with a raw pointer it has to be given."""
     _check_cache("hs2_paged_evict", cache, B, kv_heads, D, dt)
-    most = B if dst_table is None else B * dst_table.shape[1]
+    if dst_table is None:
+        dst_max_pages = 0
+    elif not isinstance(dst_table, int):
+        if dst_table.dim() != 2 or dst_max_pages not in (None, dst_table.shape[1]):
+            raise Hs2Error("hs2_paged_evict", 1)
+        dst_max_pages = dst_table.shape[1]
+    elif dst_max_pages is None:
+        raise Hs2Error("hs2_paged_evict", 1)
+    most = B * dst_max_pages
     p = _tensors("hs2_paged_evict", ((dst_table, "i32", most, True),
                                      (kept, "i32", B * (topk + window), True),
                                      (new_len, "i32", B, True)))
     _check("hs2_paged_evict", load_library().hs2_paged_evict(
         ctypes.byref(cache), B, kv_heads, D, dt, topk, window, p[0],
-        0 if dst_table is None else dst_table.shape[1], p[1], p[2], _stream(stream)))
+        dst_max_pages, p[1], p[2], _stream(stream)))

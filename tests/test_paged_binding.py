@@ -148,3 +148,15 @@ def test_append_takes_rows_without_gaps(calls):
             with pytest.raises(hs2.Hs2Error):
                 append(ld=ld, **dict(dict(K=t((7, ld), BF16), V=t((7, ld), BF16)), **kw))
     assert len(calls) == 4
+
+
+def test_evict_takes_a_raw_destination_table(calls):
+    evict()
+    evict(dst_table=4096, dst_max_pages=2)
+    evict(dst_table=None)
+    assert [a[7:9] for _, a in calls][1:] == [(4096, 2), (None, 0)] and calls[0][1][8] == 2
+    for kw in (dict(dst_table=4096), dict(dst_table=t((6,), I32)),
+               dict(dst_table=t((3, 2), I32), dst_max_pages=3), dict(dst_table=t((2, 2), I32))):
+        with pytest.raises(hs2.Hs2Error):
+            evict(**kw)
+    assert len(calls) == 3

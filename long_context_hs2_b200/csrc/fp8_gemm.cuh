@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
       for (uint32_t it = warp - 1; it < total; it += 2) {
         const uint32_t s = it % SM::kStages, acc = it % A;
         // (after a wait that gave up, reported, the barriers are still met)
-        if (ok) ok = mbar_wait(&full[s], (it / SM::kStages) & 1);
+        if (ok) ok = mbar_wait_warp(&full[s], (it / SM::kStages) & 1);
         if (it >= (uint32_t)A) fg_acc_sync<CW>(acc);
         if (ok && lane == 0) {
           tc_fence_after();
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
     // while the one before it is added, so neither the barrier of a block nor the
     // tensor memory's latency is waited for where the MMAs are ahead.
     float v[2][32];
-    bool ok = mbar_wait(&acc_full[0], 0);
+    bool ok = mbar_wait_warp(&acc_full[0], 0);
     tc_fence_after();
     tmem_ld32(taddr, v[0]);
     uint32_t it = 0;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(32 * (4 + CW), 1)
             else fg_acc_sync<CW>(a);   // (in step with the issuer, which the wait was for)
             if (it + 1 < total) {
               // (after a wait that gave up, reported, the barriers are still met)
-              if (ok) ok = mbar_wait(&acc_full[an], ((it + 1) / A) & 1);
+              if (ok) ok = mbar_wait_warp(&acc_full[an], ((it + 1) / A) & 1);
               tc_fence_after();
               tmem_ld32(taddr + an * BN, v[0]);
             }
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kFsThreads, 1)
 #pragma unroll
       for (int q = 0; q < (NP + 31) / 32; ++q)
         sc[q] = p.sa[(size_t)min(m0 + q * 32 + lane, p.M - 1) * p.kb + kb0 + i] * sb[kb0 + i];
-      if (!mbar_wait(&acc_full[a], (i >> 1) & 1)) break;
+      if (!mbar_wait_warp(&acc_full[a], (i >> 1) & 1)) break;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < NP; c += 16) {
@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kFsThreads, 1)
       if (lane == 0) mbar_arrive(&acc_empty[a]);
     }
   }
+  __syncwarp();             // (warps 0 and 1: from the one lane that had work)
   cluster_wait_acquire();   // every CTA of the cluster runs
   const int col = (warp & 3) * 32 + lane;
   const int per = (NP + cs - 1) / cs;           // rows that a CTA finishes

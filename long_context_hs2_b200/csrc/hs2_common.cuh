@@ -81,6 +81,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   raise_status(kStatusTimeout);
   return false;
 }
+// mbar_wait of a whole warp: every lane has a time limit of its own, and the warp gives up as
+// one, so that what follows (named barriers count whole warps) is the same for all its lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
 
 // -------------------------------------------------------------------- TMA --
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kBrThreads, 1)
     for (long long tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++local) {
       const int acc = local & 1;
       const uint32_t use = local >> 1;
-      if (!mbar_wait(&acc_full[acc], use & 1)) break;
+      if (!mbar_wait_warp(&acc_full[acc], use & 1)) break;
       tc_fence_after();
       const long long mb = tile / p.n_layers;
       const int layer = (int)(tile % p.n_layers);

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
     }
   } else {
     // ------------------------------- epilogue warps: this CTA's partial Y^T
-    if (n_kb > 0 && mbar_wait(done, 0)) {
+    if (n_kb > 0 && mbar_wait_warp(done, 0)) {
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
 #pragma unroll
@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kBsThreads, 1)
       tmem_ld_wait();
     }
   }
+  __syncwarp();             // (warps 0 and 1: from the one lane that had work)
   cluster_wait_acquire();   // every CTA of the cluster runs
   const int col = (warp & 3) * 32 + lane;   // epilogue thread: output column of the segment
   if (warp >= 2) {

@@ -28,7 +28,7 @@ def blocks(text):
         start = m.end()
 
 
-@pytest.mark.parametrize("name", ["fp8_gemm.cuh"])
+@pytest.mark.parametrize("name", ["fp8_gemm.cuh", "bridge_gemm.cuh", "bridge_small.cuh"])
 def test_warps_give_up_as_one(name):
     with open(os.path.join(CSRC, name)) as f:
         text = re.sub(r"//[^\n]*", "", f.read())

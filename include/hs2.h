@@ -431,7 +431,7 @@ typedef struct {
  *   y = h * gamma / sqrt(mean(h^2) + eps)
  *   sum = bf16(h);  Y = bf16(y)
  *   per 128 columns: s = max|y| / 448 (1 where that is 0), Yq = E4M3(y / s),
- *     round to nearest even, y / s taken to within 2^-22 of itself
+ *     round to nearest even, y / s in fp32
  * X, R, gamma, sum, Y: bf16, [T][hidden] ([hidden] for gamma); Yq: E4M3
  * [T][hidden]; Yq_scale: fp32 [T][ceil(hidden / 128)].  sum, Y and the pair
  * Yq, Yq_scale may be NULL, not all three; sum may be R's or X's own buffer,
@@ -463,8 +463,7 @@ HS2_API hs2_status hs2_fp8_gemm(const void* A, const float* A_scale, int64_t M, 
  *   K, V: bf16, row r's [kv_heads][D] at r * ld elements (ld >= kv_heads * D,
  *         ld % 8 == 0: K and V may lie side by side in a projection's output).
  *   E4M3 caches: per row and head, scale s = max|x| / 448 (1 where that is 0),
- *         codes E4M3(x / s), round to nearest even, saturating (x / s taken to
- *         within 2^-22 of itself).
+ *         codes E4M3(x / s), round to nearest even, saturating (x / s in fp32).
  *   weight, where kept: 0 for the new positions.
  * A sequence with more new tokens than seq_len raises HS2_ERR_DEVICE; the
  * surplus rows are skipped.

@@ -36,17 +36,42 @@ struct NormParams {
   float eps;
 };
 
-// The scale of values whose largest magnitude is amax, and the factor that
-// takes them to codes.  The factor is a product's (an approximate 1 / s) instead
-// of a division per value: off by 2^-22 of the value, where a code's own rounding
-// is 2^-4.  A scale whose reciprocal would overflow is
-// flagged (`tiny`), and its values are divided.
-__device__ __forceinline__ float e4m3_scale(float amax, float& inv, bool& tiny) {
+// The scale of values whose largest magnitude is amax, and an approximate 1 / s for their
+// quotients.  Scales so small or so large that a quotient's remainder or 1 / s is not a
+// normal number (infinite ones among them) are flagged (`far`), and their values divided.
+__device__ __forceinline__ float e4m3_scale(float amax, float& inv, bool& far) {
   const float q = __fdiv_rn(amax, 448.f);
   const float s = q > 0.f ? q : 1.f;
-  tiny = s < 1e-37f;
+  far = !(s >= 0x1p-80f && s <= 0x1p100f);
   inv = fast_rcp(s);
   return s;
+}
+// a b + c and a b of two values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// Two v / s: the product with 1 / s, corrected by its remainder, which is exact (Markstein,
+// IBM J. Res. Dev. 34, 1990).  bf16 values often lie half-way between two codes, where the
+// product alone went either way.
+__device__ __forceinline__ float2 e4m3_quotients(float a, float b, float s, float inv) {
+  const float2 v = make_float2(a, b), q = mul2(v, make_float2(inv, inv));
+  const float2 rest = fma2(q, make_float2(s, s), make_float2(-a, -b));
+  return fma2(rest, make_float2(-inv, -inv), q);   // (in these signs a -0 stays one)
 }
 // Four values as E4M3 codes (round to nearest even, saturating), first one lowest.
 __device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d) {
@@ -58,12 +83,15 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float 
 }
 // v / s as codes, N values into N / 4 words.
 template <int N>
-__device__ __forceinline__ void e4m3_codes(const float* v, float s, float inv, bool tiny,
+__device__ __forceinline__ void e4m3_codes(const float* v, float s, float inv, bool far,
                                            uint32_t* w) {
-  if (!tiny) {
+  if (!far) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4)
-      w[i / 4] = e4m3_pack4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+    for (int i = 0; i < N; i += 4) {
+      const float2 a = e4m3_quotients(v[i], v[i + 1], s, inv);
+      const float2 b = e4m3_quotients(v[i + 2], v[i + 3], s, inv);
+      w[i / 4] = e4m3_pack4(a.x, a.y, b.x, b.y);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4)
@@ -169,10 +197,10 @@ __global__ void __launch_bounds__(kNormMaxThreads) add_rmsnorm_kernel(const Norm
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (live) {
         float inv;
-        bool tiny;
-        const float s = e4m3_scale(amax, inv, tiny);
+        bool far;
+        const float s = e4m3_scale(amax, inv, far);
         uint32_t w[4];
-        e4m3_codes<kNormChunk>(h[i], s, inv, tiny, w);
+        e4m3_codes<kNormChunk>(h[i], s, inv, far, w);
         *reinterpret_cast<uint4*>(p.codes + at) = make_uint4(w[0], w[1], w[2], w[3]);
         if ((c & 7) == 0) p.scale[(size_t)row * p.n_blocks + (c >> 3)] = s;
       }

@@ -172,3 +172,51 @@ def test_append_with_an_upper_bound_of_rows(lead, n_rows, fp8):
     for name, t in after.items():
         bits = lambda a: a[~touched].contiguous().view(torch.uint8)     # noqa: E731
         assert torch.equal(bits(t), bits(before[name])), name
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [1.0, 1e-30, 1e30, 3e-37])
+def test_append_writes_the_definitions_codes(D, size):
+    # bf16 values lie half-way between two codes often: one in 4,000 of these, at size 1
+    n = 3000
+    c = P.Cache([n], 64, 1, D, True, seed=72)
+    kv = (size * torch.randn(n, 2 * D, generator=torch.Generator().manual_seed(73))).bfloat16()
+    kv[5, ::3] = -0.0
+    kv[9, 7] = math.inf
+    kv[11, :] = 0
+    dev = kv.cuda()
+    start = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    hs2.hs2_paged_append(dev[:, :D], dev[:, D:], 2 * D, n, start, c.struct, 1, 1, D, c.dt)
+    assert hs2.hs2_last_device_status() == 0
+    after = c.pools()
+    rows = c.slots(0, range(n))
+    for name, x in (("k", kv[:, :D].float()), ("v", kv[:, D:].float())):
+        s = x.abs().amax(1) / 448
+        s = torch.where(s > 0, s, torch.ones_like(s))
+        codes = (x / s[:, None]).to(P.E4M3).view(torch.uint8)
+        assert torch.equal(after[name + "_scale"][rows, 0], s)
+        got = after[name].view(torch.uint8)[rows, 0]
+        bad = torch.isnan(x / s[:, None])
+        assert torch.equal(got[~bad], codes[~bad])
+        assert (got[bad] & 0x7f == 0x7f).all()
+
+
+@pytest.mark.parametrize("hidden", [48, 4096])
+def test_norm_writes_the_definitions_codes_of_powers_of_two(hidden):
+    # rows of +-1 and of halves and quarters of it have a norm and quotients that are exact but
+    # for the scale: many quotients are ties
+    g = torch.Generator().manual_seed(74)
+    x = torch.ones(200, hidden) * (torch.randint(0, 2, (200, hidden), generator=g) * 2 - 1)
+    gamma = (torch.randint(1, 256, (hidden,), generator=g) / 256).bfloat16()
+    codes = torch.empty(200, hidden, dtype=P.E4M3, device="cuda")
+    scale = torch.empty(200, -(-hidden // 128), device="cuda")
+    hs2.hs2_add_rmsnorm(x.bfloat16().cuda(), None, gamma.cuda(), 200, hidden, 0.0, None, None, codes,
+                        scale)
+    assert hs2.hs2_last_device_status() == 0
+    y = x * gamma.float()                            # mean(x^2) = 1, exactly
+    for i, part in enumerate(y.split(128, 1)):
+        s = part.abs().amax(1, keepdim=True) / 448
+        assert torch.equal(scale[:, i].cpu(), s[:, 0])
+        want = (part / s).to(P.E4M3).view(torch.uint8)
+        got = codes.cpu().view(torch.uint8)[:, i * 128:i * 128 + part.shape[1]]
+        assert torch.equal(got, want)

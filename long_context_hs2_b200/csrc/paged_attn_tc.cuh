@@ -591,7 +591,10 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
       const float* f = row_scale + (seg & 1) * NR + c0;
 #pragma unroll
       for (int i = 0; i < NC; ++i) mref[i] = l[i] = 0.f;
-      bool fresh = true;                            // no position met yet: no references
+      // rows with a reference: those that met a logit above -inf (the same in all threads of
+      // the half; the others' mref is 0)
+      constexpr uint32_t kAll = (1u << NC) - 1u;
+      uint32_t have = 0;
       const int n = w.t1 - w.t0, skip = (it0 & 1) ^ set;
       for (uint32_t it = it0 + skip; it < it0 + n; it += 2) {
         const int st = it % KN, sb = it & 3;
@@ -634,7 +637,12 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
         float top = d[0];
 #pragma unroll
         for (int i = 1; i < NC; ++i) top = fmaxf(top, d[i]);
-        const bool raise = pt_half_any(id, fresh ? top > -INFINITY : top > kPaSlack);
+        bool over = top > (have ? kPaSlack : -INFINITY);
+        if (have && have != kAll) {
+#pragma unroll
+          for (int i = 0; i < NC; ++i) over |= !(have >> i & 1u) && d[i] > -INFINITY;
+        }
+        const bool raise = pt_half_any(id, over);
         // the set's tile before is done with O^T and P^T
         if (it >= 2) wait(&pv_done[set], ph ^ 1);
         if (raise) {
@@ -650,9 +658,11 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
           if (lane < NC) at[wq * NR] = m;
           pt_half_sync(id);
           m = fmaxf(fmaxf(at[0], at[NR]), fmaxf(at[2 * NR], at[3 * NR]));
-          if (!fresh) m = fmaxf(m, 0.f);
+          const bool had = have >> (lane & (NC - 1)) & 1u;
+          const uint32_t now = __ballot_sync(0xffffffffu, had || m > -INFINITY) & kAll;
+          if (had) m = fmaxf(m, 0.f);
           if (m == -INFINITY) m = 0.f;
-          const float shrink = fresh ? 0.f : fast_exp2(-m);
+          const float shrink = had ? fast_exp2(-m) : 1.f;
           float a[NC];
 #pragma unroll
           for (int i = 0; i < NC; ++i) {
@@ -662,7 +672,7 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
             d[i] -= mi;
             l[i] *= a[i];
           }
-          if (!fresh) {
+          if (have) {
             tc_fence_after();
 #pragma unroll
             for (int term = 0; term < (FP8 ? 2 * NR : NR); term += NR) {
@@ -676,7 +686,7 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
           }
-          fresh = false;
+          have = now;
         }
         // P
 #pragma unroll
@@ -751,7 +761,7 @@ __global__ void __launch_bounds__(PtSmem<NR, FP8>::kThreads, 1)
         float m = mref[0];
 #pragma unroll
         for (int i = 1; i < NC; ++i) m = lane == i ? mref[i] : m;
-        if (wq == 0 && lane < NC) ref[set * NR + c0 + lane] = fresh ? -INFINITY : m;
+        if (wq == 0 && lane < NC) ref[set * NR + c0 + lane] = have >> lane & 1u ? m : -INFINITY;
       }
       float o[NC];
       if (n > skip) {                                // the set had a tile

@@ -37,10 +37,13 @@ def queries(B, H, D, seed=1):
     return q.bfloat16()
 
 
-def check(c, q, o, lse):
+def check(c, q, o, lse, size=40):
+    # a logit of magnitude `size` is off by 16 * 2^-24 of it (4e-5 of 40); log2 and the sums by
+    # 6e-5 more
+    eps = 16 * 2.0 ** -24 * size + 6e-5
     eo, el, gain, mass, _ = P.attention(c, q, c.D ** -0.5)
-    assert (lse.double() - el).abs().max() <= 1e-4
-    tol = 2.0 ** -8 * eo.abs() + (2.0 ** -8 + 1e-4) * mass
+    assert (lse.double() - el).abs().max() <= eps
+    tol = 2.0 ** -8 * eo.abs() + (2.0 ** -8 + eps) * mass
     assert ((o.double() - eo).abs() <= tol).all(), ((o.double() - eo).abs() / tol).max()
     return gain
 
@@ -220,3 +223,37 @@ def test_norm_writes_the_definitions_codes_of_powers_of_two(hidden):
         want = (part / s).to(P.E4M3).view(torch.uint8)
         got = codes.cpu().view(torch.uint8)[:, i * 128:i * 128 + part.shape[1]]
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,page", PATHS)
+def test_logits_that_overflow_for_one_row(D, page, fp8):
+    # the first keys are out of row 0's reach (its logit with them is below fp32's range, the
+    # other rows' is small), and its logits with the others are all near -400
+    c = P.Cache([900], page, 1, D, fp8, seed=75)
+    k = 0.5 * torch.randn(900, D, generator=torch.Generator().manual_seed(76))
+    k[:, 0] = 0
+    k[:, 1] = -400 * math.sqrt(D) / 8
+    far = torch.zeros(900, dtype=torch.bool)
+    far[:500] = True
+    far[700] = True
+    rows = c.slots(0, range(900))
+    if fp8:
+        codes, scale = P.quantise(k)
+        codes.view(torch.uint8)[far] = 0
+        codes.view(torch.uint8)[far, 0] = 0xfe               # -448
+        scale[far] = 1e36
+        c.kc.view(torch.uint8)[rows, 0] = codes.view(torch.uint8)
+        c.ks[rows] = scale.float()
+        c.k64[rows, 0] = codes.double() * scale.float().double()
+    else:
+        k[far] = 0
+        k[far, 0] = -3e38
+        c.kc[rows, 0] = k.bfloat16()
+        c.k64[rows, 0] = k.bfloat16().double()
+    c.upload()
+    q = torch.randn(1, 32, D, generator=torch.Generator().manual_seed(77))
+    q[0, :, :2] = 0
+    q[0, 0, 0] = 256
+    q[0, :5, 1] = 8
+    check(c, q.bfloat16(), *P.run_attention(c, q.bfloat16(), D ** -0.5), size=420)

@@ -379,8 +379,7 @@ __device__ __forceinline__ void pa_load_q(const __nv_bfloat16* q, int G, uint8_t
       // (its logits are infinite or NaN, its probabilities NaN)
       const int e = amax > 0.f ? max(-126, min(126, (int)(__float_as_uint(amax) >> 23) - 127)) : 0;
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      const float down = amax < INFINITY ? __uint_as_float((uint32_t)(127 - e) << 23)
-                                         : __uint_as_float(0x7fffffffu);
+      const float down = fmaf(amax, 0.f, __uint_as_float((uint32_t)(127 - e) << 23));
       if (ch == 0) row_scale[r] = up;
       // column c of 16 goes to place: c = 4 t + i, place = 2 t + (i & 1) + 8 (i >> 1)
 #pragma unroll
@@ -809,9 +808,9 @@ __device__ __forceinline__ float pa_item_lse(const PagedAttnParams& p, int b, in
 #pragma unroll 8
   for (int c = parts.x; c <= parts.y; ++c) {
     const float2 v = p.part_ml[(size_t)(c * 2 + (c == parts.x)) * p.G + lane];
-    if (v.y == 0.f) continue;   // no positions
     const float m = fmaxf(top, v.x);
-    sum = sum * fast_exp2(top - m) + v.y * fast_exp2(v.x - m);   // (NaN stays, m = -inf too)
+    const float s = sum * fast_exp2(top - m) + v.y * fast_exp2(v.x - m);   // (NaN stays)
+    sum = v.y == 0.f ? sum : s;   // no positions (selected, not jumped over: loads in one go)
     top = m;
   }
   return top + log2f(sum);

@@ -294,10 +294,9 @@ __device__ __forceinline__ void pt_stage_q(const __nv_bfloat16* q, int G, uint8_
 #pragma unroll
         for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const int e = amax > 0.f ? max(-110, (int)(__float_as_uint(amax) >> 23) - 127) : 0;
-        // 2^(7 - e); NaN for a row with an infinity, which the saturating conversion would
-        // make 448 of (its logits are infinite or NaN, its probabilities NaN)
-        const float down = e < 128 ? __uint_as_float((uint32_t)(134 - e) << 23)
-                                   : __uint_as_float(0x7fffffffu);
+        // 2^(7 - e), + 0 * amax: NaN for a row with an infinity, which the saturating
+        // conversion would make 448 of (its logits are infinite or NaN, its probabilities NaN)
+        const float down = fmaf(amax, 0.f, __uint_as_float((uint32_t)(134 - e) << 23));
         if (ch == 0) row_scale[r] = __uint_as_float((uint32_t)(120 + e) << 23);
         uint32_t t1[2] = {0, 0}, t2[2] = {0, 0};
 #pragma unroll

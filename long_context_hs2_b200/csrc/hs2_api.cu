@@ -445,7 +445,7 @@ hs2_status run_sparse(SparseParams p, cudaStream_t s) {
 
 extern "C" {
 
-int hs2_version(void) { return 101; }
+int hs2_version(void) { return 102; }
 
 hs2_status hs2_set_fault_injection(unsigned extra_arrivals, unsigned long long wait_limit_ns) {
   t_barrier_extra = extra_arrivals;

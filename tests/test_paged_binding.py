@@ -160,3 +160,9 @@ def test_evict_takes_a_raw_destination_table(calls):
         with pytest.raises(hs2.Hs2Error):
             evict(**kw)
     assert len(calls) == 3
+
+
+def test_the_version_counts_the_paged_entry_points():
+    from long_context_hs2_b200 import build
+    build.build()
+    assert hs2.load_library().hs2_version() >= 102      # 101 had none of them

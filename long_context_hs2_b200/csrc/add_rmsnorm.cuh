@@ -6,8 +6,8 @@
 //
 // One pass: a row's values stay in registers between the sum of squares and
 // the output, so every input is read once and every output written once, and
-// HBM bounds it (131,072 x 4096 with residual to E4M3: 579 us, 6.5 TB/s, 0.99 of the
-// copy rate; 8 rows: 2.1 us, a launch).  A thread owns chunks of 16 columns (two 16-byte loads of X
+// HBM bounds it (131,072 x 4096 with residual to E4M3: 534 us in a replayed graph, 7.1 TB/s
+// with the tail of the writes in L2; 8 rows: 2.4 us, a launch).  A thread owns chunks of 16 columns (two 16-byte loads of X
 // and of R, one 16-byte store of codes); a block of 128 columns is then 8
 // neighbouring lanes, and its maximum three shuffles.  h is kept in fp32 for
 // the norm: the sum's rounding to bf16 goes to the residual stream only.

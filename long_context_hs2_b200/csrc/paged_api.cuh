@@ -94,7 +94,7 @@ hs2_status run_paged_attn(const CUtensorMap& km, const CUtensorMap& vm, const Pa
   auto kw = paged_weight_kernel<MT, D, FP8>;
   hs2_status st;
   // tcgen05 for head_dim 128 where a page's rows are a TMA box of whole swizzle atoms (4 x
-  // 256K E4M3: 85 us against 122 with warp MMAs; 8 x up to 32K bf16: 18 against 30)
+  // 256K E4M3: 86 us against 122 with warp MMAs; 8 x up to 32K bf16: 18 against 30)
   if (D == 128 && p.c.page_shift >= 3) {
     using ST = PtSmem<16 * MT, FP8>;
     auto k = paged_attn_tc_kernel<16 * MT, FP8>;
@@ -177,7 +177,7 @@ hs2_status hs2_fp8_gemm(const void* A, const float* A_scale, int64_t M, const vo
   p.K = K;
   p.kb = (K + kFgBK - 1) / kFgBK;
   cudaStream_t s = (cudaStream_t)stream;
-  // Few rows: the whole machine streams B (8 rows x 1536 x 4096: 5.3 us against 12.0 with
+  // Few rows: the whole machine streams B (8 rows x 1536 x 4096: 5.5 us against 12.0 with
   // the tiles of many rows; 64 rows: 12.3 us against 10.9, so not from there on).
   if (M <= 16) return run_fp8_gemm_small<16>(A, B, p, s);
   if (M <= 32) return run_fp8_gemm_small<32>(A, B, p, s);
@@ -351,8 +351,10 @@ hs2_status hs2_paged_evict(const hs2_paged_cache* cache, int B, int kv_heads, in
   p.topk = topk;
   p.window = window;
   p.row_bytes = kv_heads * D * (fp8 ? 1 : 2);
-  // the largest clusters that are all resident at once, with one CTA per SM: 15 of 8 fit on
-  // 148 SMs (26 sequences of 667: 20.5 us in clusters of 8, two waves, 10.9 of 4)
+  // the largest clusters that are all resident at once, with one CTA per SM, as if five
+  // sixths of the SMs took them: on 148 SMs 15 of 8 fit and 16 do not (1,216 positions: 14 us
+  // in clusters of 4, 23 of 8), 31 of 4 would and 34 do not (31 sequences: 18 us in clusters of
+  // 2, 15 of 4, 57 and 25 of 32K; 34 sequences: 18 and 26)
   int cs = kEvMaxCluster;
   while (cs > 1 && B * cs > sm_count() * 5 / 6) cs /= 2;
   p.cs = cs;

@@ -4,7 +4,7 @@
 // work, the join, and the kernels on warp MMAs, which serve head_dim 64 and pages
 // under 8 positions (777 positions, 8 heads x 64: 7.7 us with the join).  Larger
 // pages of head_dim 128: paged_attn_tc.cuh (4 x 256K E4M3: 122 us with these
-// kernels, bound by the warp MMAs and the codes' conversion, 85 there).
+// kernels, bound by the warp MMAs and the codes' conversion, 86 there).
 //
 //   s_hj = scale <q_h, k_j>,  O_h = sum_j p_hj v_j,  p_hj = exp(s_hj - lse_h),
 //   lse_h = log sum_j exp(s_hj),  weight_j += sum_h p_hj        (j < seq_len)

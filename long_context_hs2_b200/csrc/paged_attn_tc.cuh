@@ -4,8 +4,8 @@
 //
 // Bound by HBM (K and V once) where a tile's work keeps up: 8 x up to 32K bf16
 // streams at the copy rate between a start and an end of 4 and 2 us; 4 x 256K E4M3
-// takes 1.4 us a tile and SM against 0.76 us of HBM time, 85 us in all (76 without V's
-// conversion, 84 with one term of P, 81 without the vote on the references).
+// takes 1.4 us a tile and SM against 0.76 us of HBM time, 86 us in all (77 without V's
+// conversion, 84 with one term of P).
 //
 // Tiles are computed transposed, 128 positions each:
 //   S^T[128 positions][rows]  = K_tile . Q^T      (M = 128 positions)

@@ -59,7 +59,9 @@ class PagedConfig:
 class PagedLayer:
     """The layer's weights, pages and buffers on the current device.  step() may be
     captured into a CUDA graph (once for a step without eviction and once for one
-    with it); lengths live on the device."""
+    with it); lengths live on the device.  `steps` counts the calls of step(), not a
+    graph's replays: whoever replays keeps the count, and replays the step with the
+    eviction once `interval` steps have passed."""
 
     def __init__(self, cfg: PagedConfig, gamma, w_q, w_kv):
         """gamma [hidden], w_q [H * D, hidden], w_kv [2 * kv_heads * D, hidden] (K rows, then

@@ -428,7 +428,7 @@ typedef struct {
  * bf16 or in E4M3 with one scale per 128 columns (the operand layout of
  * hs2_fp8_gemm).  For every row of T rows:
  *   h = X + R (R NULL: h = X), in fp32
- *   y = h * gamma / sqrt(mean(h^2) + eps)
+ *   y = h * gamma / sqrt(mean(h^2) + eps), in fp32 (the row's sum of squares too)
  *   sum = bf16(h);  Y = bf16(y)
  *   per 128 columns: s = max|y| / 448 (1 where that is 0), Yq = E4M3(y / s),
  *     round to nearest even, y / s in fp32

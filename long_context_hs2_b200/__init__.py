@@ -316,7 +316,7 @@ def _types():
 def _tensors(fn: str, specs):
     """Device pointers of (tensor, kind of element, least elements, contiguous) entries."""
     import torch
-    types = _types()
+    types = _TYPES or _types()
     dev, out = None, []
     for t, kind, least, contiguous in specs:
         if t is None or isinstance(t, int):
@@ -383,15 +383,17 @@ def hs2_fp8_gemm(A, A_scale, M, B, B_scale, N, K, C, stream=None):
                                                        _stream(stream)))
 
 
-def _row_elements(rows) -> int:
+def _row_elements(shape, stride) -> int:
     """Elements that lie one after another from the start of each row rows[r]; 0 where a row
     has gaps."""
+    if len(shape) == 2:
+        return shape[1] if stride[1] == 1 or shape[1] == 1 else 0
     n = 1
-    for size, stride in zip(reversed(rows.shape[1:]), reversed(rows.stride()[1:])):
-        if size != 1 and stride != n:
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] != 1 and stride[i] != n:
             return 0
-        n *= size
-    return n if rows.dim() > 1 else 0
+        n *= shape[i]
+    return n if len(shape) > 1 else 0
 
 
 def hs2_paged_append(K, V, ld, n_rows, row_start, cache: hs2_paged_cache, B, kv_heads, D, dt,
@@ -400,9 +402,11 @@ def hs2_paged_append(K, V, ld, n_rows, row_start, cache: hs2_paged_cache, B, kv_
     _check_cache("hs2_paged_append", cache, B, kv_heads, D, dt)
     n = n_rows * kv_heads * D
     for rows in (K, V):
-        if not isinstance(rows, int) and rows is not None and (
-                rows.shape[0] < n_rows or (n_rows > 1 and rows.stride(0) != ld)
-                or _row_elements(rows) < kv_heads * D):
+        if isinstance(rows, int) or rows is None:
+            continue
+        shape, stride = rows.shape, rows.stride()
+        if (shape[0] < n_rows or (n_rows > 1 and stride[0] != ld)
+                or _row_elements(shape, stride) < kv_heads * D):
             raise Hs2Error("hs2_paged_append", 1)
     p = _tensors("hs2_paged_append", ((K, "bf16", n, False), (V, "bf16", n, False),
                                       (row_start, "i32", B + 1, True)))

@@ -44,3 +44,18 @@ def test_evictions_from_many_long_caches(B, in_place):
     for weights in (cache_tests.HEAVY, cache_tests.ODD):
         cache_tests.evict_case(lens, 150, 10, 1, 64, 64, False, in_place, weights, seed=82 + B,
                                spare=3 * B)
+
+
+def test_the_cache_s_own_table_as_destination_is_in_place():
+    outputs = []
+    for own in (False, True):
+        c = P.Cache([500, 60, 0], 16, 2, 64, True, seed=83, weight=True, stale=1.0)
+        kept = torch.empty(3, 80, dtype=torch.int32, device="cuda")
+        hs2.hs2_paged_evict(c.struct, 3, 2, 64, c.dt, 70, 10, c.table_dev if own else None, kept,
+                            c.len_dev)
+        assert hs2.hs2_last_device_status() == 0
+        outputs.append([kept.cpu(), c.len_dev.cpu()] + [t.contiguous().view(torch.uint8)
+                                                       for t in c.pools().values()])
+    for a, b in zip(*outputs):
+        assert torch.equal(a, b)
+    assert outputs[0][1].tolist() == [80, 60, 0]
